@@ -17,6 +17,10 @@ EPI_NONE, EPI_RELU2_FWD, EPI_RELU2_BWD, EPI_ACCUM_F32 = 0, 1, 2, 3
 GEMM_A_MN_MAJOR, GEMM_B_MN_MAJOR = 1, 2
 MLP_REUSE_WEIGHT_CASTS, MLP_ACCUMULATE_WGRAD = 1, 2
 LINEAR_REUSE_WEIGHT_CAST, LINEAR_ACCUMULATE_WGRAD = 1, 2
+DTYPE_BF16, DTYPE_F32 = 0, 1
+NORM_ACCUMULATE_WGRAD = 1
+ROPE_INTERLEAVED, ROPE_INVERSE = 1, 2
+ROPE_UNSCALED, ROPE_LINEAR, ROPE_NTK, ROPE_BY_PARTS = 0, 1, 2, 3
 
 STATUS = {0: "LM_OK", 1: "LM_ERR_INVALID_ARG", 2: "LM_ERR_ALIGNMENT",
           3: "LM_ERR_UNSUPPORTED_SHAPE", 4: "LM_ERR_UNSUPPORTED_FORMAT", 5: "LM_ERR_CUDA",
@@ -33,7 +37,10 @@ EXPORTED = ["lm_fp8_amax_scale_cast", "lm_fp8_gemm", "lm_relu2_mlp_saved_bytes",
             "lm_fp8_lmhead_ce_workspace_size", "lm_fp8_lmhead_ce", "lm_fp8_gemm_ex",
             "lm_fp8_gemm_workspace_size", "lm_fp8_linear_saved_bytes",
             "lm_fp8_linear_saved_carve", "lm_fp8_linear_workspace_size", "lm_fp8_linear_fwd",
-            "lm_fp8_linear_bwd", "lm_fp8_gemm_split_plan"]
+            "lm_fp8_linear_bwd", "lm_fp8_gemm_split_plan", "lm_layernorm_fwd",
+            "lm_layernorm_workspace_size", "lm_layernorm_bwd", "lm_dropout_add_fwd",
+            "lm_dropout_add_bwd", "lm_dropout_add_layernorm_fwd",
+            "lm_dropout_add_layernorm_bwd", "lm_rope", "lm_rope_inv_freq"]
 
 
 class LmError(RuntimeError):
@@ -57,6 +64,14 @@ class SwigluSaved(ctypes.Structure):
     """Mirror of lm_swiglu_saved."""
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("Xq", "Wguq", "Wdq", "GU", "h", "hq", "scales")]
+
+
+class RopeTensor(ctypes.Structure):
+    """Mirror of lm_rope_tensor."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "y")]
+                + [(n, ctypes.c_int64) for n in
+                   ("heads", "x_batch_stride", "x_seq_stride", "x_head_stride",
+                    "y_batch_stride", "y_seq_stride", "y_head_stride")])
 
 
 def _load():
@@ -144,6 +159,27 @@ def _load():
     L.lm_fp8_linear_bwd.argtypes = [P, ctypes.POINTER(LinearSaved), i64, i64, i64, P, P, P,
                                     ctypes.c_size_t, ctypes.c_uint32, P]
     L.lm_fp8_linear_bwd.restype = st
+    f32, f64, u32, u64 = ctypes.c_float, ctypes.c_double, ctypes.c_uint32, ctypes.c_uint64
+    size = ctypes.c_size_t
+    L.lm_layernorm_fwd.argtypes = [P, i64, P, P, i64, i64, f32, i32, P, i64, P, P, P, P]
+    L.lm_layernorm_workspace_size.argtypes = [i64, i64]
+    L.lm_layernorm_workspace_size.restype = size
+    L.lm_layernorm_bwd.argtypes = [P, i64, P, i64, P, P, P, i64, i64, i32, P, i64, P, P, P, size,
+                                   u32, P]
+    L.lm_dropout_add_fwd.argtypes = [P, i64, P, i64, i64, i64, i32, f64, P, u64, P, i64, P]
+    L.lm_dropout_add_bwd.argtypes = [P, i64, i64, i64, i32, f64, P, u64, P, i64, P]
+    L.lm_dropout_add_layernorm_fwd.argtypes = [P, i64, P, i64, P, P, i64, i64, f32, i32, f64, P,
+                                               u64, P, i64, P, i64, P, P, P, P]
+    L.lm_dropout_add_layernorm_bwd.argtypes = [P, i64, P, i64, P, i64, P, P, P, i64, i64, i32, f64,
+                                               P, u64, P, i64, P, i64, P, P, P, size, u32, P]
+    L.lm_rope.argtypes = [ctypes.POINTER(RopeTensor), i32, i64, i64, i64, i64, i32, P, P, i64, f32,
+                          u32, P]
+    L.lm_rope_inv_freq.argtypes = [f64, i64, i32, f64, f64, f64, f64, ctypes.POINTER(f64),
+                                   ctypes.POINTER(f32)]
+    for fn in ("lm_layernorm_fwd", "lm_layernorm_bwd", "lm_dropout_add_fwd", "lm_dropout_add_bwd",
+               "lm_dropout_add_layernorm_fwd", "lm_dropout_add_layernorm_bwd", "lm_rope",
+               "lm_rope_inv_freq"):
+        getattr(L, fn).restype = st
     return L
 
 
@@ -359,6 +395,187 @@ def lm_fp8_lmhead_ce(X, W, labels, loss_out, dX, dW, workspace, chunk, softcap=1
                                 _p(dX), _p(dW), _p(workspace),
                                 workspace.numel() * workspace.element_size(), _stream(stream)),
            "lm_fp8_lmhead_ce")
+
+
+# ------------------------------------------- operators between the GEMMs
+_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
+
+
+def _ld(t):
+    return 0 if t is None else t.stride(0)
+
+
+def _refuse(what, why, status=1):
+    raise LmError(status, f"{what}: {why}")
+
+
+def _check_rows(what, x, *others, row_vectors=()):
+    """x and `others` (each may be None): [rows x cols] CUDA tensors of one type
+    and device whose columns are adjacent; `row_vectors`: [cols] ones.  Returns
+    (rows, cols, lm_dtype)."""
+    if x.dim() != 2 or not x.is_cuda:
+        _refuse(what, "a 2-D CUDA tensor is wanted")
+    dtype = x.dtype
+    code = _DTYPES.get(dtype)
+    if code is None:
+        _refuse(what, f"{dtype} is not supported", 4)
+    rows, cols = shape = x.shape
+    device = x.device
+    for t in (x, *others):
+        if t is not None and (t.shape != shape or t.dtype != dtype or t.device != device
+                              or (cols > 1 and t.stride(1) != 1)):
+            _refuse(what, "tensors of one shape, type and device with adjacent columns are "
+                          "wanted")
+    for t in row_vectors:
+        if t is not None and (t.dim() != 1 or t.shape[0] != cols or t.dtype != dtype
+                              or t.device != device or (cols > 1 and t.stride(0) != 1)):
+            _refuse(what, f"weight and bias are [{cols}] tensors of the same type and device")
+    return rows, cols, code
+
+
+def _check_stats(what, rows, device, *stats):
+    for t in stats:
+        if t is not None and (t.dtype != torch.float32 or t.numel() != rows or t.device != device
+                              or not t.is_contiguous()):
+            _refuse(what, f"mean and rstd are contiguous fp32 [{rows}] tensors of the same device")
+
+
+def _check_amax(what, device, amax):
+    if amax is not None and (amax.dtype != torch.float32 or amax.numel() != 1
+                             or amax.device != device):
+        _refuse(what, "amax_out is one fp32 of the same device")
+
+
+def _check_rng(what, rng, offset, device):
+    if (rng.dtype not in (torch.int64, torch.uint64) or rng.numel() != 2 or rng.device != device
+            or not rng.is_contiguous()):
+        _refuse(what, "rng is a contiguous 64-bit integer {seed, offset} of the same device")
+    if not 0 <= offset < 1 << 64:
+        _refuse(what, "offset is an unsigned 64-bit integer")
+
+
+def _check_wgrads(what, cols, x, flags, workspace, *wgrads):
+    dtype = torch.float32 if flags & NORM_ACCUMULATE_WGRAD else x.dtype
+    for t in wgrads:
+        if t is not None and (t.dim() != 1 or t.shape[0] != cols or t.dtype != dtype
+                              or t.device != x.device or (cols > 1 and t.stride(0) != 1)):
+            _refuse(what, f"dweight and dbias are [{cols}] {dtype} tensors of the same device")
+    if workspace is not None and (workspace.device != x.device or not workspace.is_contiguous()):
+        _refuse(what, "the workspace is a contiguous buffer of the same device")
+
+
+def lm_layernorm_fwd(X, weight, bias, Y, mean=None, rstd=None, eps=1e-5, amax_out=None,
+                     stream=None):
+    rows, cols, dt = _check_rows("lm_layernorm_fwd", X, Y, row_vectors=(weight, bias))
+    _check_stats("lm_layernorm_fwd", rows, X.device, mean, rstd)
+    _check_amax("lm_layernorm_fwd", X.device, amax_out)
+    _check(lib.lm_layernorm_fwd(_p(X), _ld(X), _p(weight), _p(bias), rows, cols, eps, dt, _p(Y),
+                                _ld(Y), _p(mean), _p(rstd), _p(amax_out), _stream(stream)),
+           "lm_layernorm_fwd")
+
+
+def lm_layernorm_workspace_size(rows, cols):
+    return lib.lm_layernorm_workspace_size(rows, cols)
+
+
+def lm_layernorm_bwd(dY, X, weight, mean, rstd, dX, dweight, dbias, workspace, flags=0,
+                     stream=None):
+    """dweight, dbias: [cols] of X's type, or fp32 with NORM_ACCUMULATE_WGRAD;
+    either may be None."""
+    rows, cols, dt = _check_rows("lm_layernorm_bwd", X, dY, dX, row_vectors=(weight,))
+    _check_stats("lm_layernorm_bwd", rows, X.device, mean, rstd)
+    _check_wgrads("lm_layernorm_bwd", cols, X, flags, workspace, dweight, dbias)
+    _check(lib.lm_layernorm_bwd(_p(dY), _ld(dY), _p(X), _ld(X), _p(weight), _p(mean), _p(rstd),
+                                rows, cols, dt, _p(dX), _ld(dX), _p(dweight), _p(dbias),
+                                _p(workspace), _nbytes(workspace), flags, _stream(stream)),
+           "lm_layernorm_bwd")
+
+
+def lm_dropout_add_fwd(X, residual, Y, p, rng, offset=0, stream=None):
+    rows, cols, dt = _check_rows("lm_dropout_add_fwd", X, residual, Y)
+    _check_rng("lm_dropout_add_fwd", rng, offset, X.device)
+    _check(lib.lm_dropout_add_fwd(_p(X), _ld(X), _p(residual), _ld(residual), rows, cols, dt, p,
+                                  _p(rng), offset, _p(Y), _ld(Y), _stream(stream)),
+           "lm_dropout_add_fwd")
+
+
+def lm_dropout_add_bwd(dY, dX, p, rng, offset=0, stream=None):
+    rows, cols, dt = _check_rows("lm_dropout_add_bwd", dY, dX)
+    _check_rng("lm_dropout_add_bwd", rng, offset, dY.device)
+    _check(lib.lm_dropout_add_bwd(_p(dY), _ld(dY), rows, cols, dt, p, _p(rng), offset, _p(dX),
+                                  _ld(dX), _stream(stream)), "lm_dropout_add_bwd")
+
+
+def lm_dropout_add_layernorm_fwd(X, residual, weight, bias, S, Y, p, rng, offset=0, mean=None,
+                                 rstd=None, eps=1e-5, amax_out=None, stream=None):
+    what = "lm_dropout_add_layernorm_fwd"
+    rows, cols, dt = _check_rows(what, X, residual, S, Y, row_vectors=(weight, bias))
+    _check_stats(what, rows, X.device, mean, rstd)
+    _check_amax(what, X.device, amax_out)
+    _check_rng(what, rng, offset, X.device)
+    _check(lib.lm_dropout_add_layernorm_fwd(
+        _p(X), _ld(X), _p(residual), _ld(residual), _p(weight), _p(bias), rows, cols, eps, dt, p,
+        _p(rng), offset, _p(S), _ld(S), _p(Y), _ld(Y), _p(mean), _p(rstd), _p(amax_out),
+        _stream(stream)), what)
+
+
+def lm_dropout_add_layernorm_bwd(dY, dS, S, weight, mean, rstd, p, rng, dX, dR, dweight, dbias,
+                                 workspace, offset=0, flags=0, stream=None):
+    what = "lm_dropout_add_layernorm_bwd"
+    rows, cols, dt = _check_rows(what, S, dY, dS, dX, dR, row_vectors=(weight,))
+    _check_stats(what, rows, S.device, mean, rstd)
+    _check_rng(what, rng, offset, S.device)
+    _check_wgrads(what, cols, S, flags, workspace, dweight, dbias)
+    _check(lib.lm_dropout_add_layernorm_bwd(
+        _p(dY), _ld(dY), _p(dS), _ld(dS), _p(S), _ld(S), _p(weight), _p(mean), _p(rstd), rows,
+        cols, dt, p, _p(rng), offset, _p(dX), _ld(dX), _p(dR), _ld(dR), _p(dweight), _p(dbias),
+        _p(workspace), _nbytes(workspace), flags, _stream(stream)), what)
+
+
+def lm_rope(xs, ys, inv_freq, positions=None, start=0, magnitude=1.0, flags=0, stream=None):
+    """xs, ys: one or two [batch, seq, heads, head_dim] tensors each, which share
+    all but the number of heads; inv_freq: fp64 [rot_dim / 2]; positions: int64
+    [batch, seq], or None (start + s)."""
+    if not 1 <= len(xs) <= 2 or len(ys) != len(xs) or xs[0].dim() != 4 or not xs[0].is_cuda:
+        _refuse("lm_rope", "one or two 4-D CUDA tensors and as many outputs are wanted")
+    batch, seq, _, head_dim = xs[0].shape
+    dtype, device = xs[0].dtype, xs[0].device
+    code = _DTYPES.get(dtype)
+    if code is None:
+        _refuse("lm_rope", f"{dtype} is not supported", 4)
+    if (inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or inv_freq.device != device
+            or not inv_freq.is_contiguous()):
+        _refuse("lm_rope", "inv_freq is a contiguous fp64 vector of the same device")
+    if positions is not None and (positions.dtype != torch.int64 or positions.device != device
+                                  or positions.numel() != batch * seq
+                                  or not positions.is_contiguous()):
+        _refuse("lm_rope", "positions is a contiguous int64 [batch, seq] of the same device")
+    if not -1 << 63 <= start < 1 << 63:
+        _refuse("lm_rope", "start is a signed 64-bit integer")
+    arr = (RopeTensor * len(xs))()
+    for t, x, y in zip(arr, xs, ys):
+        if (x.shape != y.shape or x.dim() != 4 or x.shape[0] != batch or x.shape[1] != seq
+                or x.shape[3] != head_dim or x.dtype != dtype or y.dtype != dtype
+                or x.device != device or y.device != device
+                or (head_dim > 1 and (x.stride(3) != 1 or y.stride(3) != 1))):
+            _refuse("lm_rope", "tensors of one type, device, batch, seq and head_dim with adjacent "
+                               "elements are wanted")
+        t.x, t.y, t.heads = x.data_ptr(), y.data_ptr(), x.shape[2]
+        t.x_batch_stride, t.x_seq_stride, t.x_head_stride, _ = x.stride()
+        t.y_batch_stride, t.y_seq_stride, t.y_head_stride, _ = y.stride()
+    _check(lib.lm_rope(arr, len(xs), batch, seq, head_dim, 2 * inv_freq.shape[0], code,
+                       _p(inv_freq), _p(positions), start, magnitude, flags, _stream(stream)),
+           "lm_rope")
+
+
+def lm_rope_inv_freq(rot_dim, theta=10000.0, scaling=ROPE_UNSCALED, factor=1.0, context=0.0,
+                     slow=1.0, fast=32.0):
+    """(frequencies, magnitude): a list of rot_dim / 2 floats, and a float
+    (host arithmetic only)."""
+    out, mag = (ctypes.c_double * max(1, rot_dim // 2))(), ctypes.c_float(0.0)
+    _check(lib.lm_rope_inv_freq(theta, rot_dim, scaling, factor, context, slow, fast, out,
+                                ctypes.byref(mag)), "lm_rope_inv_freq")
+    return list(out[:rot_dim // 2]), mag.value
 
 
 def lm_get_error(stream=None):

@@ -9,14 +9,23 @@ libfp8lm.so does every step of the computation.
     lin = api.Linear(M, K, N)            # a plain linear Y = X W^T (attention, LM head)
     Y = lin.forward(X, W)
     dX, dW = lin.backward(dY)
+
+    # between the GEMMs: layer norm, dropout into the residual stream, rotary positions
+    rng = api.dropout_rng(seed)
+    s, y, mean, rstd = api.dropout_add_layernorm(x, residual, weight, bias, 0.1, rng)
+    inv_freq, magnitude = api.rope_frequencies(head_dim)
+    q, k = api.rope([q, k], inv_freq, magnitude=magnitude)
 """
+import functools
+
 import torch
 
 from . import _lib
 from ._lib import (E4M3, E5M2, EPI_ACCUM_F32, EPI_NONE, EPI_RELU2_BWD,  # noqa: F401
                    EPI_RELU2_FWD, GEMM_A_MN_MAJOR, GEMM_B_MN_MAJOR, LINEAR_ACCUMULATE_WGRAD,
                    LINEAR_REUSE_WEIGHT_CAST, MLP_ACCUMULATE_WGRAD, MLP_REUSE_WEIGHT_CASTS,
-                   LmError)
+                   NORM_ACCUMULATE_WGRAD, ROPE_BY_PARTS, ROPE_INTERLEAVED, ROPE_INVERSE,
+                   ROPE_LINEAR, ROPE_NTK, ROPE_UNSCALED, LmError)
 
 
 def _dev(t):
@@ -347,3 +356,140 @@ def linear_fwd_bwd(X, W, dY, stream=None):
     sc = torch.cat([lin.view("scales"), lin.workspace_view("scales").view(1, 4)]).cpu().numpy()
     return Y, dX, dW, dict(Xq=lin.view("Xq"), Wq=lin.view("Wq"), dYq=lin.workspace_view("dYq"),
                            scales=sc)
+
+
+# ------------------------------------------------- operators between the GEMMs
+def _placed(fn):
+    """Runs fn on its first tensor's device and on `stream` (a torch.cuda.Stream;
+    None: that device's current one), where the outputs and workspaces are
+    allocated too."""
+    @functools.wraps(fn)
+    def placed(x, *args, stream=None, **kw):
+        device = (x[0] if isinstance(x, (list, tuple)) else x).device
+        if device.type != "cuda" or (stream is None
+                                     and device.index == torch.cuda.current_device()):
+            return fn(x, *args, **kw)
+        with torch.cuda.device(device):
+            with torch.cuda.stream(stream or torch.cuda.current_stream(device)):
+                return fn(x, *args, **kw)
+    return placed
+
+
+def _stats(x):
+    both = torch.empty(2, x.shape[0], dtype=torch.float32, device=x.device)
+    return both[0], both[1]
+
+
+def _wgrads(x, dweight, dbias, accumulate):
+    """dweight, dbias and the workspace of a norm's backward."""
+    rows, cols = x.shape
+    if not accumulate:
+        if dweight is None:
+            dweight = torch.empty(cols, dtype=x.dtype, device=x.device)
+        if dbias is None:
+            dbias = torch.empty(cols, dtype=x.dtype, device=x.device)
+    ws = torch.empty(_lib.lm_layernorm_workspace_size(rows, cols), dtype=torch.uint8,
+                     device=x.device)
+    return dweight, dbias, ws
+
+
+@_placed
+def layernorm(x, weight=None, bias=None, eps=1e-5, out=None, amax_out=None):
+    """Layer norm of [rows x cols] bf16 or fp32.  Returns (y, mean, rstd), the
+    statistics fp32 [rows] for layernorm_backward.  amax_out: a zeroed fp32
+    that receives max |y|, the amax_in of a following cast()."""
+    y = torch.empty_like(x) if out is None else out
+    mean, rstd = _stats(x)
+    _lib.lm_layernorm_fwd(x, weight, bias, y, mean, rstd, eps, amax_out)
+    return y, mean, rstd
+
+
+@_placed
+def layernorm_backward(dy, x, weight, mean, rstd, out=None, dweight=None, dbias=None,
+                       accumulate=False):
+    """Returns (dx, dweight, dbias), the latter two of x's type.  With accumulate,
+    dweight and dbias are given fp32 accumulators (or None) that are added to."""
+    dx = torch.empty_like(x) if out is None else out
+    dweight, dbias, ws = _wgrads(x, dweight, dbias, accumulate)
+    _lib.lm_layernorm_bwd(dy, x, weight, mean, rstd, dx, dweight, dbias, ws,
+                          NORM_ACCUMULATE_WGRAD if accumulate else 0)
+    return dx, dweight, dbias
+
+
+def dropout_rng(seed, offset=0, device="cuda"):
+    """The device {seed, offset} that the dropout calls read.  A training loop
+    adds to rng[1] between steps (also between replays of a captured graph);
+    calls of one step differ by their `offset` argument."""
+    signed = [v - (1 << 64) if v >= 1 << 63 else v for v in (seed, offset)]
+    return torch.tensor(signed, dtype=torch.int64, device=device)
+
+
+@_placed
+def dropout_add(x, p, rng, offset=0, residual=None, out=None):
+    """residual + dropout(x) (plain dropout without a residual)."""
+    y = torch.empty_like(x) if out is None else out
+    _lib.lm_dropout_add_fwd(x, residual, y, p, rng, offset)
+    return y
+
+
+@_placed
+def dropout_add_backward(dy, p, rng, offset=0, out=None):
+    """dx of dropout_add (the residual's gradient is dy itself)."""
+    dx = torch.empty_like(dy) if out is None else out
+    _lib.lm_dropout_add_bwd(dy, dx, p, rng, offset)
+    return dx
+
+
+@_placed
+def dropout_add_layernorm(x, residual, weight, bias, p, rng, offset=0, eps=1e-5, amax_out=None):
+    """s = residual + dropout(x) and its layer norm y in one pass.  Returns
+    (s, y, mean, rstd)."""
+    s, y = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd = _stats(x)
+    _lib.lm_dropout_add_layernorm_fwd(x, residual, weight, bias, s, y, p, rng, offset, mean, rstd,
+                                      eps, amax_out)
+    return s, y, mean, rstd
+
+
+@_placed
+def dropout_add_layernorm_backward(dy, ds, s, weight, mean, rstd, p, rng, offset=0, dweight=None,
+                                   dbias=None, accumulate=False):
+    """From dy and ds (the gradient of s from the stream after it, or None):
+    (dx, dresidual, dweight, dbias)."""
+    dx, dr = torch.empty_like(s), torch.empty_like(s)
+    dweight, dbias, ws = _wgrads(s, dweight, dbias, accumulate)
+    _lib.lm_dropout_add_layernorm_bwd(dy, ds, s, weight, mean, rstd, p, rng, dx, dr, dweight,
+                                      dbias, ws, offset,
+                                      NORM_ACCUMULATE_WGRAD if accumulate else 0)
+    return dx, dr, dweight, dbias
+
+
+def rope_frequencies(rot_dim, theta=10000.0, scaling=ROPE_UNSCALED, factor=1.0, context=0.0,
+                     slow=1.0, fast=32.0, device="cuda"):
+    """(inv_freq, magnitude) for rope(): an fp64 device vector of rot_dim / 2
+    frequencies, kept by the caller, and a float."""
+    freqs, magnitude = _lib.lm_rope_inv_freq(rot_dim, theta, scaling, factor, context, slow, fast)
+    return torch.tensor(freqs, dtype=torch.float64, device=device), magnitude
+
+
+def _rope(xs, inv_freq, positions, start, interleaved, magnitude, out, flags):
+    ys = [torch.empty_like(x) for x in xs] if out is None else out
+    _lib.lm_rope(xs, ys, inv_freq, positions, start, magnitude,
+                 flags | (ROPE_INTERLEAVED if interleaved else 0))
+    return ys
+
+
+@_placed
+def rope(xs, inv_freq, positions=None, start=0, interleaved=False, magnitude=1.0, out=None):
+    """Rotary positions of one or two [batch, seq, heads, head_dim] tensors (Q and
+    K), any strides but adjacent elements; the first 2 len(inv_freq) elements of
+    each head turn.  positions: int64 [batch, seq], or None for start + s.
+    Returns the list of outputs (`out` may be `xs`: in place)."""
+    return _rope(xs, inv_freq, positions, start, interleaved, magnitude, out, 0)
+
+
+@_placed
+def rope_backward(dys, inv_freq, positions=None, start=0, interleaved=False, magnitude=1.0,
+                  out=None):
+    """The gradients of rope()'s inputs from those of its outputs."""
+    return _rope(dys, inv_freq, positions, start, interleaved, magnitude, out, ROPE_INVERSE)

@@ -205,6 +205,175 @@ LM_API lm_status lm_rmsnorm_fp8_cast(const void* R, const void* weight, int64_t 
                                      float* amax_out, float* scale_out, float* inv_scale_out,
                                      uint8_t* q, uint8_t* qT, lm_stream_t stream);
 
+/* Element type of the row operators below (layer norm, dropout, rotary
+ * positions): all tensors of one call share it. */
+typedef enum { LM_DTYPE_BF16 = 0, LM_DTYPE_F32 = 1 } lm_dtype;
+
+#define LM_NORM_ACCUMULATE_WGRAD 1u /* dweight and dbias are fp32 accumulators; this
+                                       call's sums are added to them */
+
+/*
+ * Layer norm (J. Ba, J. Kiros, G. Hinton, "Layer normalization", 2016), the
+ * producer of a GEMM input in models that centre their pre-norm:
+ *
+ *   m = mean_c X[r][c],  v = mean_c (X[r][c] - m)^2,  rstd = 1 / sqrt(v + eps)
+ *   Y[r][c] = (X[r][c] - m) rstd weight[c] + bias[c]
+ *
+ * Sums in fp32, the variance from the centred values; Y is rounded once.
+ * X, Y: [rows x cols] with row strides ldx, ldy (elements, >= cols); weight,
+ * bias: [cols], each may be NULL (1 and 0); mean, rstd: fp32 [rows] for the
+ * backward pass, each may be NULL.
+ * amax_out: device fp32 or NULL.  If non-NULL it is max-reduced (atomically,
+ *   order independent) with max |Y|, NaN above everything, so that
+ *   lm_fp8_amax_scale_cast can take it as amax_in and skip its reduction pass.
+ *   The caller zeroes it before the first call that feeds it.
+ * Any rows >= 0 and cols >= 1; pointers need their element's alignment
+ *   only.  Whole 8-column accesses are used where cols and all row strides are
+ *   multiples of 8 and all pointers of 8 elements' bytes.  Y may be X (same
+ *   pointer and stride); no other overlap.  Columns past cols are not touched.
+ */
+LM_API lm_status lm_layernorm_fwd(const void* X, int64_t ldx, const void* weight,
+                                  const void* bias, int64_t rows, int64_t cols, float eps,
+                                  lm_dtype dtype, void* Y, int64_t ldy, float* mean, float* rstd,
+                                  float* amax_out, lm_stream_t stream);
+
+/* Bytes of scratch lm_layernorm_bwd and lm_dropout_add_layernorm_bwd need for
+ * the weight gradients' partial sums; 0 for an unsupported shape. */
+LM_API size_t lm_layernorm_workspace_size(int64_t rows, int64_t cols);
+
+/*
+ * Layer norm backward, with h = (X - m) rstd and g = dY weight:
+ *   dX = rstd (g - mean_c g - h mean_c(g h))
+ *   dweight[c] = sum_r dY h,  dbias[c] = sum_r dY
+ * mean, rstd: as the forward wrote them.  dweight, dbias: [cols] of the
+ * tensors' type, or fp32 accumulators with LM_NORM_ACCUMULATE_WGRAD; either
+ * may be NULL, and with both NULL no workspace is needed.  The sums over the
+ * rows have a fixed order: the same inputs give the same bits.
+ * workspace: device scratch of >= lm_layernorm_workspace_size bytes, 16-byte
+ *   aligned.  Calls that share a workspace must not overlap on the GPU.
+ * dX may be dY or X (same pointer and stride).  rows == 0 gives zero gradients.
+ */
+LM_API lm_status lm_layernorm_bwd(const void* dY, int64_t lddy, const void* X, int64_t ldx,
+                                  const void* weight, const float* mean, const float* rstd,
+                                  int64_t rows, int64_t cols, lm_dtype dtype, void* dX,
+                                  int64_t lddx, void* dweight, void* dbias, void* workspace,
+                                  size_t ws_bytes, uint32_t flags, lm_stream_t stream);
+
+/*
+ * Dropout of a branch, added to the residual stream:
+ *
+ *   Y[r][c] = residual[r][c] + (keep(r, c) ? X[r][c] scale : 0)
+ *
+ * residual may be NULL (plain dropout).  The mask is never stored: element (r, c)
+ * is kept where halfword c % 8 of Philox4x32-10 (J. Salmon et al., "Parallel
+ * random numbers: as easy as 1, 2, 3", 2011) at counter
+ * {c / 8, r, lo(o), hi(o)} under the key `seed` is at least drop = p 2^16
+ * (rounded to nearest, ties to even); scale = 2^16 / (2^16 - drop), the
+ * factor of the rounded p.  The product and the sum are rounded to fp32 one
+ * after the other, the sum to Y's type.  With drop = 2^16 (p within 2^-17 of
+ * 1) everything is dropped.  A dropped element contributes 0 whatever X holds.
+ * p in [0, 1].  rng: device {seed, offset}, read by the kernel, so that a
+ *   captured graph takes a new mask when the caller advances the offset; o is that
+ *   offset plus the argument `offset` (the layer's number, for instance).
+ * X, residual, Y: [rows x cols] with row strides; alignment as
+ *   lm_layernorm_fwd.  Y may be X or residual (same pointer and stride).
+ */
+LM_API lm_status lm_dropout_add_fwd(const void* X, int64_t ldx, const void* residual, int64_t ldr,
+                                    int64_t rows, int64_t cols, lm_dtype dtype, double p,
+                                    const uint64_t* rng, uint64_t offset, void* Y, int64_t ldy,
+                                    lm_stream_t stream);
+
+/* Its backward: dX[r][c] = keep(r, c) ? dY[r][c] scale : 0 with the mask of the
+ * same p, rng and offset (the residual's gradient is dY itself).  dX may be dY. */
+LM_API lm_status lm_dropout_add_bwd(const void* dY, int64_t lddy, int64_t rows, int64_t cols,
+                                    lm_dtype dtype, double p, const uint64_t* rng,
+                                    uint64_t offset, void* dX, int64_t lddx, lm_stream_t stream);
+
+/*
+ * The end of one branch and the start of the next in one pass:
+ *   S = residual + dropout(X)    as lm_dropout_add_fwd
+ *   Y = layer norm of S          as lm_layernorm_fwd on the S that is stored
+ * S may be X or residual (same pointer and stride).
+ */
+LM_API lm_status lm_dropout_add_layernorm_fwd(const void* X, int64_t ldx, const void* residual,
+                                              int64_t ldr, const void* weight, const void* bias,
+                                              int64_t rows, int64_t cols, float eps,
+                                              lm_dtype dtype, double p, const uint64_t* rng,
+                                              uint64_t offset, void* S, int64_t lds, void* Y,
+                                              int64_t ldy, float* mean, float* rstd,
+                                              float* amax_out, lm_stream_t stream);
+
+/*
+ * Its backward, from dY and the gradient dS that reaches S from the residual
+ * stream after it (NULL: none):
+ *   dR = dS + (lm_layernorm_bwd's dX of dY at S)
+ *   dX = keep ? dR scale : 0     (from dR before it is rounded)
+ *   dweight, dbias, workspace, flags as lm_layernorm_bwd.
+ * dX and dR may each be one of dY, dS and S (same pointer and stride), and are
+ * not the same.
+ */
+LM_API lm_status lm_dropout_add_layernorm_bwd(
+    const void* dY, int64_t lddy, const void* dS, int64_t ldds, const void* S, int64_t lds,
+    const void* weight, const float* mean, const float* rstd, int64_t rows, int64_t cols,
+    lm_dtype dtype, double p, const uint64_t* rng, uint64_t offset, void* dX, int64_t lddx,
+    void* dR, int64_t lddr, void* dweight, void* dbias, void* workspace, size_t ws_bytes,
+    uint32_t flags, lm_stream_t stream);
+
+/* One tensor of lm_rope: [batch, seq, heads, head_dim], the last dimension
+ * contiguous, the others at any strides (elements).  The strides of x are not
+ * negative; those of y give every head elements of its own. */
+typedef struct lm_rope_tensor {
+    const void* x;
+    void* y;
+    int64_t heads;
+    int64_t x_batch_stride, x_seq_stride, x_head_stride;
+    int64_t y_batch_stride, y_seq_stride, y_head_stride;
+} lm_rope_tensor;
+
+#define LM_ROPE_INTERLEAVED 1u /* pair i is elements 2i, 2i + 1; else i, i + rot_dim / 2 */
+#define LM_ROPE_INVERSE 2u     /* the backward pass: the sine negated */
+
+/*
+ * Rotary positions (J. Su et al., "RoFormer", 2021; decomputer.nl, "Het trainen
+ * van een 3.8B LLM tot 0.384 CORE voor $998", "Appendix: De configuratie",
+ * theta 10000) of one or two tensors, Q and K, in one launch.  Pair i of the
+ * first rot_dim elements of each head turns by a = position inv_freq[i]:
+ *
+ *   (x1, x2) -> magnitude (x1 cos a - x2 sin a, x2 cos a + x1 sin a)
+ *
+ * and the other elements are copied.  The angle is reduced in fp64, the
+ * rotation is fp32.  With LM_ROPE_INVERSE x is the gradient of the output and y
+ * that of the input.
+ * inv_freq: device fp64 [rot_dim / 2], 8-byte aligned (lm_rope_inv_freq).
+ * positions: device int64 [batch x seq], or NULL: token s of each sequence is
+ *   at start + s.
+ * rot_dim even, 0 <= rot_dim <= head_dim <= 65536; batch x seq < 2^31; heads x
+ *   head_dim < 2^30; x and y need their element's alignment only.
+ *   batch, seq or heads may be 0.  y may be x (same pointer and strides).
+ */
+LM_API lm_status lm_rope(const lm_rope_tensor* tensors, int count, int64_t batch, int64_t seq,
+                         int64_t head_dim, int64_t rot_dim, lm_dtype dtype,
+                         const double* inv_freq, const int64_t* positions, int64_t start,
+                         float magnitude, uint32_t flags, lm_stream_t stream);
+
+/* How the frequencies are changed for a context `factor` times longer. */
+typedef enum {
+    LM_ROPE_UNSCALED = 0,
+    LM_ROPE_LINEAR = 1,  /* positions interpolated: every frequency / factor */
+    LM_ROPE_NTK = 2,     /* theta factor^(rot_dim / (rot_dim - 2)) */
+    LM_ROPE_BY_PARTS = 3 /* by the turns a pair makes over the original context: below
+                            `slow` / factor, above `fast` unchanged, blended between;
+                            magnitude 0.1 ln(factor) + 1 (B. Peng et al., "YaRN",
+                            2023, sections 3.2 and 3.4) */
+} lm_rope_scaling;
+
+/* Host arithmetic in fp64 (no GPU): inv_freq[i] = theta^(-2i / rot_dim), scaled,
+ * for i < rot_dim / 2 into HOST memory, and the magnitude for lm_rope (1 but
+ * for LM_ROPE_BY_PARTS).  factor >= 1; context, slow < fast: LM_ROPE_BY_PARTS only. */
+LM_API lm_status lm_rope_inv_freq(double theta, int64_t rot_dim, lm_rope_scaling scaling,
+                                  double factor, double context, double slow, double fast,
+                                  double* inv_freq, float* magnitude);
+
 /*
  * Tensors the relu^2 MLP forward saves for its backward.  Every pointer is a
  * caller-owned device buffer (see lm_relu2_mlp_saved_carve).  Shapes for
@@ -469,8 +638,9 @@ LM_API lm_status lm_get_error(lm_stream_t stream, uint32_t* where_out);
  * next recorded event therefore brackets launch i.  lm_timing_detach()
  * stops recording and returns the number of events recorded.
  * lm_timing_kinds() copies one character per recorded launch ('a' amax
- * reduction, 'c' cast, 's' scales only, 'g' GEMM, 'n' RMSNorm, 'w'
- * SwiGLU backward elementwise, 'e' softcapped CE, 'l' mean loss) into out[0..cap) and
+ * reduction, 'c' cast, 's' scales only, 'g' GEMM, 'n' RMSNorm or layer norm, 'w'
+ * SwiGLU backward elementwise, 'e' softcapped CE, 'l' mean loss, 'd' dropout,
+ * 'r' rotary positions) into out[0..cap) and
  * returns how many it wrote; labels are kept for the first 4096 launches
  * after an attach.  State is per host thread.
  */
