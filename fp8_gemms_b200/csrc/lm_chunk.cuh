@@ -34,6 +34,9 @@ struct Elem<f32_t> {
 
 constexpr int kChunk = 8;               // columns of a lane
 constexpr int kWarpCols = 32 * kChunk;  // columns of a warp's chunks
+// Columns are counted in 32 bits; the last chunk's may pass the row's end by
+// less than a block's 8192.
+constexpr int64_t kMaxCols = int64_t(1) << 30;
 
 template <typename T>
 struct Chunk {
@@ -52,6 +55,49 @@ __device__ __forceinline__ float get(const Chunk<bf16_t>& c, int j) {
 }
 __device__ __forceinline__ float get(const Chunk<f32_t>& c, int j) {
     return __uint_as_float(c.w[j]);
+}
+// Two fp32 in one register pair: the packed instructions do two IEEE operations in one
+// issue slot.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 make_f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float lo_of(F2 a) { return __uint_as_float((uint32_t)a.v); }
+__device__ __forceinline__ float hi_of(F2 a) { return __uint_as_float((uint32_t)(a.v >> 32)); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+// Elements 2 i and 2 i + 1 of a chunk, and back.
+constexpr int kPairs = kChunk / 2;
+__device__ __forceinline__ F2 get2(const Chunk<bf16_t>& c, int i) {
+    return make_f2(__uint_as_float(c.w[i] << 16), __uint_as_float(c.w[i] & 0xFFFF0000u));
+}
+__device__ __forceinline__ F2 get2(const Chunk<f32_t>& c, int i) {
+    return make_f2(__uint_as_float(c.w[2 * i]), __uint_as_float(c.w[2 * i + 1]));
+}
+__device__ __forceinline__ void put2(Chunk<bf16_t>& c, int i, F2 v) {
+    c.w[i] = pack_bf16(lo_of(v), hi_of(v));
+}
+__device__ __forceinline__ void put2(Chunk<f32_t>& c, int i, F2 v) {
+    c.w[2 * i] = __float_as_uint(lo_of(v));
+    c.w[2 * i + 1] = __float_as_uint(hi_of(v));
 }
 __device__ __forceinline__ void put(Chunk<bf16_t>& c, const float (&v)[kChunk]) {
 #pragma unroll
@@ -89,54 +135,57 @@ __device__ __forceinline__ void st_vec(void* p, const Chunk<f32_t>& c) {
 
 // The column of element j of this lane's chunk.
 template <bool VEC>
-__device__ __forceinline__ int64_t chunk_col(int64_t base, int lane, int j) {
+__device__ __forceinline__ int chunk_col(int base, int lane, int j) {
     return VEC ? base + kChunk * lane + j : base + 32 * j + lane;
 }
 
 // Whether this lane has a whole chunk (VEC), or any element of one, in a row
-// of `cols` columns.
-template <bool VEC>
-__device__ __forceinline__ bool chunk_has(int64_t base, int lane, int64_t cols) {
-    return chunk_col<VEC>(base, lane, 0) < cols;
+// of `cols` columns.  FULL: every lane has one (known when compiled).
+template <bool VEC, bool FULL = false>
+__device__ __forceinline__ bool chunk_has(int base, int lane, int cols) {
+    return FULL || chunk_col<VEC>(base, lane, 0) < cols;
 }
 
 // This lane's chunk of the 256 columns at `base` of a row (nothing is read and
 // the elements are zero past `cols`).
-template <typename T, bool VEC>
-__device__ __forceinline__ Chunk<T> load_chunk(const void* row, int64_t base, int lane,
-                                               int64_t cols) {
+template <typename T, bool VEC, bool FULL = false>
+__device__ __forceinline__ Chunk<T> load_chunk(const void* row, int base, int lane, int cols) {
     using raw = typename Elem<T>::raw;
     const raw* p = static_cast<const raw*>(row);
     Chunk<T> c;
-#pragma unroll
-    for (int i = 0; i < Elem<T>::kWords; ++i) c.w[i] = 0u;
-    if constexpr (VEC) {
-        if (chunk_has<true>(base, lane, cols)) ld_vec(c, p + base + kChunk * lane);
+    if constexpr (FULL) {
+        ld_vec(c, p + base + kChunk * lane);
     } else {
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) {
-            const int64_t col = base + 32 * j + lane;
-            const uint32_t v = col < cols ? (uint32_t)p[col] : 0u;
-            if constexpr (sizeof(raw) == 4)
-                c.w[j] = v;
-            else
-                c.w[j >> 1] |= v << (16 * (j & 1));
+        for (int i = 0; i < Elem<T>::kWords; ++i) c.w[i] = 0u;
+        if constexpr (VEC) {
+            if (chunk_has<true>(base, lane, cols)) ld_vec(c, p + base + kChunk * lane);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j) {
+                const int col = base + 32 * j + lane;
+                const uint32_t v = col < cols ? (uint32_t)p[col] : 0u;
+                if constexpr (sizeof(raw) == 4)
+                    c.w[j] = v;
+                else
+                    c.w[j >> 1] |= v << (16 * (j & 1));
+            }
         }
     }
     return c;
 }
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void store_chunk(void* row, int64_t base, int lane, int64_t cols,
+template <typename T, bool VEC, bool FULL = false>
+__device__ __forceinline__ void store_chunk(void* row, int base, int lane, int cols,
                                             const Chunk<T>& c) {
     using raw = typename Elem<T>::raw;
     raw* p = static_cast<raw*>(row);
     if constexpr (VEC) {
-        if (chunk_has<true>(base, lane, cols)) st_vec(p + base + kChunk * lane, c);
+        if (chunk_has<true, FULL>(base, lane, cols)) st_vec(p + base + kChunk * lane, c);
     } else {
 #pragma unroll
         for (int j = 0; j < kChunk; ++j) {
-            const int64_t col = base + 32 * j + lane;
+            const int col = base + 32 * j + lane;
             if (col < cols) {
                 if constexpr (sizeof(raw) == 4)
                     p[col] = c.w[j];
@@ -148,8 +197,9 @@ __device__ __forceinline__ void store_chunk(void* row, int64_t base, int lane, i
 }
 
 template <typename T>
-__device__ __forceinline__ const void* row_at(const void* base, int64_t row, int64_t ld) {
-    return static_cast<const typename Elem<T>::raw*>(base) + row * ld;
+__device__ __forceinline__ const void* row_at(const void* base, int64_t row, int64_t ld,
+                                              int col = 0) {
+    return static_cast<const typename Elem<T>::raw*>(base) + row * ld + col;
 }
 template <typename T>
 __device__ __forceinline__ void* row_at(void* base, int64_t row, int64_t ld) {

@@ -19,42 +19,82 @@ struct DropArgs {
     Dropout drop;
 };
 
-// A warp takes 256 columns of a row at a time.
+// Tiles of a warp: 16 KB of loads a block for either type.
+template <typename T>
+__host__ __device__ constexpr int tiles_of_warp() {
+    return sizeof(typename Elem<T>::raw) == 2 ? 4 : 2;
+}
+
+// A tile is 256 columns of a row, or with VEC and rows of at most 128 columns as
+// many whole rows as a warp has lanes for.  A warp takes a few tiles that follow one
+// another, loads them all, and makes the masks while the loads are on their way.
+// `across`: tiles of a row; `rows_in`: rows of a tile.
 template <typename T, bool VEC, bool ADD>
-__global__ void __launch_bounds__(256) dropout_kernel(const DropArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int64_t tiles_c = (a.cols + kWarpCols - 1) / kWarpCols;
-    const int64_t tiles = a.rows * tiles_c;
-    const PhiloxKey key = philox_key(a.drop);
-    for (int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); t < tiles;
-         t += (int64_t)gridDim.x * 8) {
-        const int64_t row = t / tiles_c, base = (t - row * tiles_c) * kWarpCols;
-        Chunk<T> c = load_chunk<T, VEC>(row_at<T>(a.x, row, a.ldx), base, lane, a.cols), r;
-        if (ADD) r = load_chunk<T, VEC>(row_at<T>(a.residual, row, a.ldr), base, lane, a.cols);
-        const uint32_t keep = keep_bits<VEC>(key, a.drop.drop, row, base, lane);
-        float v[kChunk];
+__global__ void __launch_bounds__(256) dropout_kernel(const DropArgs a, int across, int rows_in) {
+    constexpr int kTiles = tiles_of_warp<T>();
+    const int lane = threadIdx.x & 31, cols = (int)a.cols, groups = cols >> 3;
+    const int sub = rows_in > 1 ? lane / groups : 0;
+    const int group = rows_in > 1 ? lane - sub * groups : lane;
+    const int64_t first = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kTiles;
+    int64_t row = first / across;
+    int tile = (int)(first - row * across);
+    row = row * rows_in + sub;
+    Chunk<T> c[kTiles], r[kTiles];
+    int64_t at[kTiles];
+    int base[kTiles];
+    bool has[kTiles];
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) {
-            v[j] = (keep >> j) & 1 ? __fmul_rn(get(c, j), a.drop.scale) : 0.f;
-            if (ADD) v[j] = __fadd_rn(get(r, j), v[j]);
+    for (int k = 0; k < kTiles; ++k) {
+        at[k] = row;
+        base[k] = tile * kWarpCols;
+        const bool in = row < a.rows;
+        has[k] = VEC ? in && sub < rows_in && base[k] + kChunk * group < cols : in;
+        if (VEC) {
+            if (has[k]) {
+                ld_vec(c[k], row_at<T>(a.x, row, a.ldx, base[k] + kChunk * group));
+                if (ADD) ld_vec(r[k], row_at<T>(a.residual, row, a.ldr, base[k] + kChunk * group));
+            }
+        } else if (in) {
+            c[k] = load_chunk<T, VEC>(row_at<T>(a.x, row, a.ldx), base[k], lane, cols);
+            if (ADD) r[k] = load_chunk<T, VEC>(row_at<T>(a.residual, row, a.ldr), base[k], lane, cols);
         }
-        put(c, v);
-        store_chunk<T, VEC>(row_at<T>(a.y, row, a.ldy), base, lane, a.cols, c);
+        if (++tile == across) tile = 0, row += rows_in;
+    }
+    const PhiloxKey key = philox_key(a.drop);
+    const F2 scale = make_f2(a.drop.scale, a.drop.scale);
+#pragma unroll
+    for (int k = 0; k < kTiles; ++k) {
+        const Keep<VEC> keep = keep_at<VEC>(key, a.drop, (uint32_t)at[k],
+                                            (uint32_t)(base[k] >> 3) + group, lane);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+            const F2 v = kept(mul2(get2(c[k], j), scale), keep, a.drop, j);
+            put2(c[k], j, ADD ? add2(get2(r[k], j), v) : v);
+        }
+        if (VEC) {
+            if (has[k])
+                st_vec(static_cast<char*>(row_at<T>(a.y, at[k], a.ldy)) +
+                           (int64_t)(base[k] + kChunk * group) * sizeof(typename Elem<T>::raw),
+                       c[k]);
+        } else if (has[k]) {
+            store_chunk<T, VEC>(row_at<T>(a.y, at[k], a.ldy), base[k], lane, cols, c[k]);
+        }
     }
 }
 
 template <typename T, bool ADD>
 lm_status launch(const DropArgs& a, bool vec, cudaStream_t s) {
-    const int sms = sm_count();
-    if (sms <= 0) return LM_ERR_CUDA;
-    const int64_t tiles = a.rows * ((a.cols + kWarpCols - 1) / kWarpCols);
-    const int64_t want = (tiles + 7) / 8, most = (int64_t)sms * 8;
-    const unsigned grid = (unsigned)(want < most ? want : most);
+    constexpr int kTiles = tiles_of_warp<T>();
+    const int across = (int)((a.cols + kWarpCols - 1) / kWarpCols);
+    const int rows_in = vec && a.cols <= 128 ? (int)(256 / a.cols) : 1;
+    const int64_t tiles = (a.rows + rows_in - 1) / rows_in * across;
+    const int64_t blocks = (tiles + 8 * kTiles - 1) / (8 * kTiles);
+    if (blocks >= (int64_t(1) << 31)) return LM_ERR_UNSUPPORTED_SHAPE;
     timing_mark(s, 'd');
     if (vec)
-        dropout_kernel<T, true, ADD><<<grid, 256, 0, s>>>(a);
+        dropout_kernel<T, true, ADD><<<(unsigned)blocks, 256, 0, s>>>(a, across, rows_in);
     else
-        dropout_kernel<T, false, ADD><<<grid, 256, 0, s>>>(a);
+        dropout_kernel<T, false, ADD><<<(unsigned)blocks, 256, 0, s>>>(a, across, rows_in);
     return launch_status();
 }
 

@@ -18,14 +18,19 @@
 
 #include <stdint.h>
 
+#include "lm_chunk.cuh"
+
 namespace lm {
 namespace {
 
 struct Dropout {
     const uint64_t* rng;  // device {seed, offset}
     uint64_t offset;      // added to the offset on the device
-    uint32_t drop;        // 0..65536: halfwords below it are dropped
-    float scale;          // 65536 / (65536 - drop); 0 where everything is dropped
+    // drop = 0..65536: halfwords below it are dropped.  It is held as what each half of a
+    // word is compared with, min(drop, 65535) twice, and what the word is first masked
+    // with: all ones, or zero for drop = 65536, so that nothing is kept.
+    uint32_t least, live;
+    float scale;  // 65536 / (65536 - drop); 0 where everything is dropped
 };
 
 // The key and the offset's halves, read once by each thread.
@@ -36,6 +41,16 @@ struct PhiloxKey {
 __device__ __forceinline__ PhiloxKey philox_key(const Dropout& d) {
     const uint64_t seed = d.rng[0], off = d.rng[1] + d.offset;
     return {(uint32_t)seed, (uint32_t)(seed >> 32), (uint32_t)off, (uint32_t)(off >> 32)};
+}
+
+// The same key, without what the compiler would keep of it across a loop: the ten
+// rounds' keys are made again (two additions a round) instead of held in 20
+// registers, for kernels that have none to spare.
+__device__ __forceinline__ PhiloxKey renewed(const PhiloxKey& key) {
+    PhiloxKey k = key;
+    asm volatile("mov.b32 %0, %1;" : "=r"(k.k0) : "r"(key.k0));
+    asm volatile("mov.b32 %0, %1;" : "=r"(k.k1) : "r"(key.k1));
+    return k;
 }
 
 __device__ __forceinline__ void philox(const PhiloxKey& key, uint32_t c0, uint32_t c1,
@@ -54,29 +69,63 @@ __device__ __forceinline__ void philox(const PhiloxKey& key, uint32_t c0, uint32
     out[0] = c0, out[1] = c1, out[2] = c2, out[3] = c3;
 }
 
-// Bit j: whether element j of this lane's chunk stays.  base: the first of the
-// warp's 256 columns (a multiple of 256).  Every lane of the warp calls it: without
-// VEC each lane makes the bits of columns base + 8 lane .. + 7, and the bits
-// that its own elements, base + 32 j + lane, need come from other lanes.
+// Which elements of this lane's chunk stay.  VEC: the lane's own four words.  Otherwise
+// lane l makes the words of columns base + 8 l .. + 7, while its own elements are columns
+// base + 32 j + l, whose bits come from other lanes: bit j of `bits`.
 template <bool VEC>
-__device__ __forceinline__ uint32_t keep_bits(const PhiloxKey& key, uint32_t drop, int64_t row,
-                                              int64_t base, int lane) {
+struct Keep;
+template <>
+struct Keep<true> {
     uint32_t w[4];
-    philox(key, (uint32_t)(base >> 3) + lane, (uint32_t)row, w);
-    uint32_t m = 0;
+};
+template <>
+struct Keep<false> {
+    uint32_t bits;
+};
+
+// group: the row's eighth column group that this lane makes the words of, base / 8 + lane
+// for the warp's 256 columns at `base`.  Every lane calls it.
+template <bool VEC>
+__device__ __forceinline__ Keep<VEC> keep_at(const PhiloxKey& key, const Dropout& d, uint32_t row,
+                                             uint32_t group, int lane) {
+    uint32_t w[4];
+    philox(key, group, row, w);
+    Keep<VEC> k;
+    if constexpr (VEC) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t h = (j & 1) ? w[j >> 1] >> 16 : w[j >> 1] & 0xFFFFu;
-        m |= (h >= drop ? 1u : 0u) << j;
-    }
-    if (VEC) return m;
-    uint32_t own = 0;
+        for (int i = 0; i < 4; ++i) k.w[i] = w[i] & d.live;
+    } else {
+        uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t g = __shfl_sync(0xFFFFFFFFu, m, 4 * j + (lane >> 3));
-        own |= ((g >> (lane & 7)) & 1u) << j;
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t h = ((j & 1) ? w[j >> 1] >> 16 : w[j >> 1] & 0xFFFFu) & d.live;
+            m |= (h >= (d.least & 0xFFFFu) ? 1u : 0u) << j;
+        }
+        k.bits = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t g = __shfl_sync(0xFFFFFFFFu, m, 4 * j + (lane >> 3));
+            k.bits |= ((g >> (lane & 7)) & 1u) << j;
+        }
     }
-    return own;
+    return k;
+}
+
+template <bool VEC>
+__device__ __forceinline__ Keep<VEC> keep_of(const PhiloxKey& key, const Dropout& d, uint32_t row,
+                                             int base, int lane) {
+    return keep_at<VEC>(key, d, row, (uint32_t)(base >> 3) + lane, lane);
+}
+
+// Elements 2 i and 2 i + 1 of the chunk, zero where dropped.
+__device__ __forceinline__ F2 kept(F2 v, const Keep<true>& k, const Dropout& d, int i) {
+    bool hi, lo;
+    __vibmax_u16x2(k.w[i], d.least, &hi, &lo);  // each half >= `least`
+    return make_f2(lo ? lo_of(v) : 0.f, hi ? hi_of(v) : 0.f);
+}
+__device__ __forceinline__ F2 kept(F2 v, const Keep<false>& k, const Dropout&, int i) {
+    return make_f2((k.bits >> (2 * i)) & 1 ? lo_of(v) : 0.f,
+                   (k.bits >> (2 * i + 1)) & 1 ? hi_of(v) : 0.f);
 }
 
 }  // namespace

@@ -4,6 +4,7 @@
 
 #include <math.h>
 
+#include "lm_chunk.cuh"
 #include "lm_internal.h"
 #include "lm_philox.cuh"
 
@@ -15,7 +16,7 @@ inline bool aligned_to(const void* p, unsigned bytes) {
 }
 
 inline bool too_large(int64_t rows, int64_t cols) {
-    return rows >= (int64_t(1) << 31) || cols >= (int64_t(1) << 31);
+    return rows >= (int64_t(1) << 31) || cols > kMaxCols;
 }
 
 struct RowTensor {
@@ -52,8 +53,11 @@ inline lm_status dropout_args(double p, const uint64_t* rng, uint64_t offset, Dr
     if (!aligned_to(rng, 8)) return LM_ERR_ALIGNMENT;
     d->rng = rng;
     d->offset = offset;
-    d->drop = (uint32_t)lrint(p * 65536.0);
-    d->scale = d->drop < 65536u ? (float)(65536.0 / (65536.0 - d->drop)) : 0.f;
+    const uint32_t drop = (uint32_t)lrint(p * 65536.0);
+    const uint32_t half = drop < 65535u ? drop : 65535u;
+    d->least = half << 16 | half;
+    d->live = drop < 65536u ? 0xFFFFFFFFu : 0u;
+    d->scale = drop < 65536u ? (float)(65536.0 / (65536.0 - drop)) : 0.f;
     return LM_OK;
 }
 

@@ -227,7 +227,7 @@ typedef enum { LM_DTYPE_BF16 = 0, LM_DTYPE_F32 = 1 } lm_dtype;
  *   order independent) with max |Y|, NaN above everything, so that
  *   lm_fp8_amax_scale_cast can take it as amax_in and skip its reduction pass.
  *   The caller zeroes it before the first call that feeds it.
- * Any rows >= 0 and cols >= 1; pointers need their element's alignment
+ * 0 <= rows < 2^31, 1 <= cols <= 2^30, strides < 2^31; pointers need their element's alignment
  *   only.  Whole 8-column accesses are used where cols and all row strides are
  *   multiples of 8 and all pointers of 8 elements' bytes.  Y may be X (same
  *   pointer and stride); no other overlap.  Columns past cols are not touched.
@@ -347,8 +347,8 @@ typedef struct lm_rope_tensor {
  * inv_freq: device fp64 [rot_dim / 2], 8-byte aligned (lm_rope_inv_freq).
  * positions: device int64 [batch x seq], or NULL: token s of each sequence is
  *   at start + s.
- * rot_dim even, 0 <= rot_dim <= head_dim <= 65536; batch x seq < 2^31; heads x
- *   head_dim < 2^30; x and y need their element's alignment only.
+ * rot_dim even, 0 <= rot_dim <= head_dim <= 512; batch x seq < 2^31; heads <=
+ *   65536 a tensor; x and y need their element's alignment only.
  *   batch, seq or heads may be 0.  y may be x (same pointer and strides).
  */
 LM_API lm_status lm_rope(const lm_rope_tensor* tensors, int count, int64_t batch, int64_t seq,
