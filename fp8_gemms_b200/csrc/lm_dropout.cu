@@ -25,7 +25,60 @@ __host__ __device__ constexpr int tiles_of_warp() {
     return sizeof(typename Elem<T>::raw) == 2 ? 4 : 2;
 }
 
-// A tile is 256 columns of a row, or with VEC and rows of at most 128 columns as
+// One chunk: y = (residual +) (keep ? x scale : 0), in place of c.
+template <bool ADD, typename T, bool VEC>
+__device__ __forceinline__ void drop_chunk(Chunk<T>& c, const Chunk<T>& r, const Keep<VEC>& keep,
+                                           const Dropout& d) {
+    const F2 scale = make_f2(d.scale, d.scale);
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) {
+        const F2 v = kept(mul2(get2(c, j), scale), keep, d, j);
+        put2(c, j, ADD ? add2(get2(r, j), v) : v);
+    }
+}
+
+// Rows of a whole number of warps' work (kTiles x 256 columns): a warp takes that many
+// columns of one row, with no tests and one address.  The generator and the
+// selections bound this kernel (the ALU pipe), so every instruction counts.
+template <typename T, bool ADD>
+__global__ void __launch_bounds__(256) dropout_full_kernel(const DropArgs a, uint32_t across) {
+    constexpr int kTiles = tiles_of_warp<T>();
+    __shared__ uint2 keys[10];
+    const int lane = threadIdx.x & 31;
+    const int64_t task = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int64_t row = task >> 32 == 0 ? (uint32_t)task / across : task / across;
+    const int first = (int)(task - row * across) * kTiles * kWarpCols;
+    const bool in = row < a.rows;
+    Chunk<T> c[kTiles], r[kTiles];
+    if (in) {
+        const void* const x = row_at<T>(a.x, row, a.ldx, first);
+        const void* const res = ADD ? row_at<T>(a.residual, row, a.ldr, first) : nullptr;
+#pragma unroll
+        for (int k = 0; k < kTiles; ++k) {
+            c[k] = load_chunk<T, true, true>(x, k * kWarpCols, lane, 0);
+            if (ADD) r[k] = load_chunk<T, true, true>(res, k * kWarpCols, lane, 0);
+        }
+    }
+    // beside a residual there are no registers for the rounds' keys
+    const auto key = [&] {
+        if constexpr (ADD)
+            return philox_key(a.drop);
+        else
+            return PhiloxRounds(a.drop, keys);
+    }();
+    if (!in) return;
+    char* const y = static_cast<char*>(row_at<T>(a.y, row, a.ldy)) +
+                    (int64_t)first * sizeof(typename Elem<T>::raw);
+#pragma unroll
+    for (int k = 0; k < kTiles; ++k) {
+        const Keep<true> keep = keep_at<true>(key, a.drop, (uint32_t)row,
+                                              (uint32_t)(first >> 3) + 32 * k + lane, lane);
+        drop_chunk<ADD>(c[k], r[k], keep, a.drop);
+        store_chunk<T, true, true>(y, k * kWarpCols, lane, 0, c[k]);
+    }
+}
+
+// Any rows.  A tile is 256 columns of a row, or with VEC and rows of at most 128 columns as
 // many whole rows as a warp has lanes for.  A warp takes a few tiles that follow one
 // another, loads them all, and makes the masks while the loads are on their way.
 // `across`: tiles of a row; `rows_in`: rows of a tile.
@@ -36,7 +89,7 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropArgs a, int acro
     const int sub = rows_in > 1 ? lane / groups : 0;
     const int group = rows_in > 1 ? lane - sub * groups : lane;
     const int64_t first = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kTiles;
-    int64_t row = first / across;
+    int64_t row = first >> 32 == 0 ? (uint32_t)first / (uint32_t)across : first / across;
     int tile = (int)(first - row * across);
     row = row * rows_in + sub;
     Chunk<T> c[kTiles], r[kTiles];
@@ -61,16 +114,11 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropArgs a, int acro
         if (++tile == across) tile = 0, row += rows_in;
     }
     const PhiloxKey key = philox_key(a.drop);
-    const F2 scale = make_f2(a.drop.scale, a.drop.scale);
 #pragma unroll
     for (int k = 0; k < kTiles; ++k) {
         const Keep<VEC> keep = keep_at<VEC>(key, a.drop, (uint32_t)at[k],
                                             (uint32_t)(base[k] >> 3) + group, lane);
-#pragma unroll
-        for (int j = 0; j < kPairs; ++j) {
-            const F2 v = kept(mul2(get2(c[k], j), scale), keep, a.drop, j);
-            put2(c[k], j, ADD ? add2(get2(r[k], j), v) : v);
-        }
+        drop_chunk<ADD>(c[k], r[k], keep, a.drop);
         if (VEC) {
             if (has[k])
                 st_vec(static_cast<char*>(row_at<T>(a.y, at[k], a.ldy)) +
@@ -85,6 +133,13 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropArgs a, int acro
 template <typename T, bool ADD>
 lm_status launch(const DropArgs& a, bool vec, cudaStream_t s) {
     constexpr int kTiles = tiles_of_warp<T>();
+    if (vec && a.cols % (kTiles * kWarpCols) == 0) {
+        const int64_t across = a.cols / (kTiles * kWarpCols), blocks = (a.rows * across + 7) / 8;
+        if (blocks >= (int64_t(1) << 31)) return LM_ERR_UNSUPPORTED_SHAPE;
+        timing_mark(s, 'd');
+        dropout_full_kernel<T, ADD><<<(unsigned)blocks, 256, 0, s>>>(a, (uint32_t)across);
+        return launch_status();
+    }
     const int across = (int)((a.cols + kWarpCols - 1) / kWarpCols);
     const int rows_in = vec && a.cols <= 128 ? (int)(256 / a.cols) : 1;
     const int64_t tiles = (a.rows + rows_in - 1) / rows_in * across;

@@ -394,9 +394,9 @@ __host__ __device__ constexpr int bwd_threads() {
 
 // The backward pass, every tensor read once for dx and the weight gradients.  A thread
 // keeps its NCH chunks' sums over its rows in registers; at the end the block adds its
-// groups' sums and writes one part of the partial sums.  The rows and the weight are
-// in shared memory and read from there for each of the two sweeps, which leaves the
-// registers to the sums and to more warps.
+// groups' sums and writes one part of the partial sums.  With four chunks a thread the
+// sums leave no registers for the row and the weight: they are read from shared
+// memory again for the second sweep.
 // VEC: rows come by asynchronous copies, `stages` - 1 ahead; otherwise by scalar loads, one
 // at a time.
 template <typename T, bool VEC, int NCH, bool DROP, bool FULL>
@@ -407,6 +407,7 @@ __global__ void __launch_bounds__(bwd_threads<T, NCH>(), 1)
     constexpr int NT = DROP ? 3 : 2;
     constexpr int kSlot = Slots<T>::kBytes, kRow = NT * NCH * kSlot;  // of a warp
     constexpr int kSize = sizeof(typename Elem<T>::raw), kNext = kWarpCols * kSize;
+    constexpr bool kAgain = NCH > 2;  // read the row and the weight again for the second sweep
     const int cols = (int)a.cols;
     const Group g(warps);
     const int first = g.warp * NCH * kWarpCols;
@@ -415,11 +416,12 @@ __global__ void __launch_bounds__(bwd_threads<T, NCH>(), 1)
     const Slots<T> ws(smem, g.warp * NCH * kSlot, g.lane);
     const Slots<T> slots(smem, warps * NCH * kSlot + (g.group * warps + g.warp) * stages * kRow,
                          g.lane);
-    if (g.group == 0) {
+    Chunk<T> w[NCH], d[NCH], c[NCH];
 #pragma unroll
-        for (int i = 0; i < NCH; ++i)
-            ws.put(0, i, a.weight ? load_chunk<T, VEC>(a.weight, first + i * kWarpCols, g.lane, cols)
-                                  : ones_chunk<T>());
+    for (int i = 0; i < NCH; ++i) {
+        w[i] = a.weight ? load_chunk<T, VEC>(a.weight, first + i * kWarpCols, g.lane, cols)
+                        : ones_chunk<T>();
+        if (kAgain && g.group == 0) ws.put(0, i, w[i]);
     }
     F2 dw[NCH][kPairs] = {}, db[NCH][kPairs] = {};
     PhiloxKey key{};
@@ -504,12 +506,13 @@ __global__ void __launch_bounds__(bwd_threads<T, NCH>(), 1)
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
             if (NCH > 2 && i == 2) __syncwarp();  // or the compiler loads all four, and spills
-            const Chunk<T> d = slots.take(at, i), c = slots.take(at, NCH + i), w = ws.take(0, i);
+            d[i] = slots.take(at, i), c[i] = slots.take(at, NCH + i);
+            if (kAgain) w[i] = ws.take(0, i);
 #pragma unroll
             for (int j = 0; j < kPairs; ++j) {
                 // past the columns dy is 0, so the sums get nothing from there
-                const F2 y = get2(d, j), wj = get2(w, j);
-                const F2 t = mul2(y, add2(get2(c, j), minus_mean));
+                const F2 y = get2(d[i], j), wj = get2(w[i], j);
+                const F2 t = mul2(y, add2(get2(c[i], j), minus_mean));
                 s1 = fma2(y, wj, s1);
                 s2 = fma2(t, wj, s2);
                 dw[i][j] = fma2(t, r2, dw[i][j]);
@@ -519,6 +522,7 @@ __global__ void __launch_bounds__(bwd_threads<T, NCH>(), 1)
         float c1 = lo_of(s1) + hi_of(s1), c2 = (lo_of(s2) + hi_of(s2)) * rstd;
         group_sum2(g, buf + mine, c1, c2);
         mine ^= 64;
+        if (!kAgain) as_stored(d), as_stored(c), as_stored(w);
         // dx = rstd g - rstd c1 - (x - mean) rstd (rstd c2)
         const float per = (float)a.inv_cols * rstd;
         c1 *= per, c2 = c2 * per * rstd;
@@ -527,14 +531,17 @@ __global__ void __launch_bounds__(bwd_threads<T, NCH>(), 1)
         for (int i = 0; i < NCH; ++i) {
             const int base = first + i * kWarpCols;
             if (NCH > 2 && i == 2) __syncwarp();  // or the compiler loads all four, and spills
-            const Chunk<T> d = slots.take(at, i), c = slots.take(at, NCH + i), w = ws.take(0, i);
+            if (kAgain) {
+                d[i] = slots.take(at, i), c[i] = slots.take(at, NCH + i);
+                w[i] = ws.take(0, i);
+            }
             Chunk<T> up, out;
             if (has_ds) up = slots.take(at, 2 * NCH + i);
             F2 v[kPairs];
 #pragma unroll
             for (int j = 0; j < kPairs; ++j) {
-                v[j] = fma2(mul2(get2(d, j), get2(w, j)), r2, m1);
-                v[j] = fma2(add2(get2(c, j), minus_mean), m2, v[j]);
+                v[j] = fma2(mul2(get2(d[i], j), get2(w[i], j)), r2, m1);
+                v[j] = fma2(add2(get2(c[i], j), minus_mean), m2, v[j]);
                 if (has_ds) v[j] = add2(get2(up, j), v[j]);
                 put2(out, j, v[j]);
             }

@@ -26,9 +26,9 @@ namespace {
 struct Dropout {
     const uint64_t* rng;  // device {seed, offset}
     uint64_t offset;      // added to the offset on the device
-    // drop = 0..65536: halfwords below it are dropped.  It is held as what each half of a
-    // word is compared with, min(drop, 65535) twice, and what the word is first masked
-    // with: all ones, or zero for drop = 65536, so that nothing is kept.
+    // drop = 0..65536: halfwords below it are dropped.  It is held as what the upper half of a
+    // word is compared with, min(drop, 65535) << 16, and whether anything is kept (0 for
+    // drop = 65536).
     uint32_t least, live;
     float scale;  // 65536 / (65536 - drop); 0 where everything is dropped
 };
@@ -53,18 +53,40 @@ __device__ __forceinline__ PhiloxKey renewed(const PhiloxKey& key) {
     return k;
 }
 
-__device__ __forceinline__ void philox(const PhiloxKey& key, uint32_t c0, uint32_t c1,
-                                       uint32_t (&out)[4]) {
-    uint32_t c2 = key.o0, c3 = key.o1, k0 = key.k0, k1 = key.k1;
+// The ten rounds' keys in registers, for kernels that have 20 to spare: made once a block
+// and read from shared memory, or the compiler makes them again for each chunk.
+struct PhiloxRounds {
+    uint32_t k0[10], k1[10], o0, o1;
+    // `keys`: shared, for one block; every thread calls it.
+    __device__ __forceinline__ PhiloxRounds(const Dropout& d, uint2 (&keys)[10]) {
+        const PhiloxKey key = philox_key(d);
+        o0 = key.o0, o1 = key.o1;
+        if (threadIdx.x < 10)
+            keys[threadIdx.x] = make_uint2(key.k0 + threadIdx.x * 0x9E3779B9u,
+                                           key.k1 + threadIdx.x * 0xBB67AE85u);
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < 10; ++r)
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                         : "=r"(k0[r]), "=r"(k1[r])
+                         : "r"((uint32_t)__cvta_generic_to_shared(&keys[r])));
+    }
+};
+__device__ __forceinline__ uint32_t round_key0(const PhiloxKey& k, int r) { return k.k0 + r * 0x9E3779B9u; }
+__device__ __forceinline__ uint32_t round_key1(const PhiloxKey& k, int r) { return k.k1 + r * 0xBB67AE85u; }
+__device__ __forceinline__ uint32_t round_key0(const PhiloxRounds& k, int r) { return k.k0[r]; }
+__device__ __forceinline__ uint32_t round_key1(const PhiloxRounds& k, int r) { return k.k1[r]; }
+
+template <typename Key>
+__device__ __forceinline__ void philox(const Key& key, uint32_t c0, uint32_t c1, uint32_t (&out)[4]) {
+    uint32_t c2 = key.o0, c3 = key.o1;
 #pragma unroll
     for (int r = 0; r < 10; ++r) {
         const uint64_t a = (uint64_t)0xD2511F53u * c0, b = (uint64_t)0xCD9E8D57u * c2;
-        c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+        c0 = (uint32_t)(b >> 32) ^ c1 ^ round_key0(key, r);
         c1 = (uint32_t)b;
-        c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+        c2 = (uint32_t)(a >> 32) ^ c3 ^ round_key1(key, r);
         c3 = (uint32_t)a;
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
     }
     out[0] = c0, out[1] = c1, out[2] = c2, out[3] = c3;
 }
@@ -85,21 +107,23 @@ struct Keep<false> {
 
 // group: the row's eighth column group that this lane makes the words of, base / 8 + lane
 // for the warp's 256 columns at `base`.  Every lane calls it.
-template <bool VEC>
-__device__ __forceinline__ Keep<VEC> keep_at(const PhiloxKey& key, const Dropout& d, uint32_t row,
+template <bool VEC, typename Key>
+__device__ __forceinline__ Keep<VEC> keep_at(const Key& key, const Dropout& d, uint32_t row,
                                              uint32_t group, int lane) {
     uint32_t w[4];
     philox(key, group, row, w);
     Keep<VEC> k;
     if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) k.w[i] = w[i] & d.live;
+        for (int i = 0; i < 4; ++i) k.w[i] = w[i];
     } else {
         uint32_t m = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint32_t h = ((j & 1) ? w[j >> 1] >> 16 : w[j >> 1] & 0xFFFFu) & d.live;
-            m |= (h >= (d.least & 0xFFFFu) ? 1u : 0u) << j;
+            // the upper half as it is (what is below does not change the comparison), the
+            // lower half moved up
+            const uint32_t h = (j & 1) ? w[j >> 1] : w[j >> 1] << 16;
+            m |= (h >= d.least && d.live ? 1u : 0u) << j;
         }
         k.bits = 0;
 #pragma unroll
@@ -119,9 +143,8 @@ __device__ __forceinline__ Keep<VEC> keep_of(const PhiloxKey& key, const Dropout
 
 // Elements 2 i and 2 i + 1 of the chunk, zero where dropped.
 __device__ __forceinline__ F2 kept(F2 v, const Keep<true>& k, const Dropout& d, int i) {
-    bool hi, lo;
-    __vibmax_u16x2(k.w[i], d.least, &hi, &lo);  // each half >= `least`
-    return make_f2(lo ? lo_of(v) : 0.f, hi ? hi_of(v) : 0.f);
+    return make_f2((k.w[i] << 16) >= d.least && d.live ? lo_of(v) : 0.f,
+                   k.w[i] >= d.least && d.live ? hi_of(v) : 0.f);
 }
 __device__ __forceinline__ F2 kept(F2 v, const Keep<false>& k, const Dropout&, int i) {
     return make_f2((k.bits >> (2 * i)) & 1 ? lo_of(v) : 0.f,

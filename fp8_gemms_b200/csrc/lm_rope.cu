@@ -10,6 +10,8 @@
 // t = position * inv_freq / 2 pi, and only t - rint(t) goes to fp32, so the
 // rotation is right at any position; no table is kept or read.  The other
 // head_dim - rot_dim elements are copied (not touched in place).
+#include <type_traits>
+
 #include "lm_chunk.cuh"
 #include "lm_internal.h"
 #include "lm_rows.h"
@@ -20,7 +22,7 @@ namespace {
 struct RopeArgs {
     lm_rope_tensor t[2];
     int64_t batch, seq, tokens;
-    int heads0, heads, head_dim, rot_dim;
+    int heads0, heads, head_dim, rot_dim;  // heads: of both tensors
     const double* inv_freq;
     const int64_t* positions;
     int64_t start;
@@ -39,10 +41,10 @@ __device__ __forceinline__ float2 cos_sin(double position, double inv_freq, floa
     return make_float2(c * magnitude, s * magnitude * sign);
 }
 
-// V elements that follow one another: V = 8 is a chunk, V = 1 a scalar.
+// V elements that follow one another: V = 8 is a chunk, 2 a word or two, 1 a scalar.
 template <typename T, int V>
 struct Run {
-    float v[V];
+    uint32_t w[V == 8 ? Elem<T>::kWords : V == 2 && Elem<T>::kWords == 8 ? 2 : 1];
 };
 template <typename T, int V>
 __device__ __forceinline__ void load_run(Run<T, V>& r, const void* p) {
@@ -50,170 +52,237 @@ __device__ __forceinline__ void load_run(Run<T, V>& r, const void* p) {
         Chunk<T> c;
         ld_vec(c, p);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r.v[i] = get(c, i);
-    } else if constexpr (sizeof(typename Elem<T>::raw) == 4) {
-        r.v[0] = *static_cast<const float*>(p);
+        for (int i = 0; i < Elem<T>::kWords; ++i) r.w[i] = c.w[i];
+    } else if constexpr (V * sizeof(typename Elem<T>::raw) == 8) {
+        const uint2 u = *static_cast<const uint2*>(p);
+        r.w[0] = u.x, r.w[1] = u.y;
+    } else if constexpr (V * sizeof(typename Elem<T>::raw) == 4) {
+        r.w[0] = *static_cast<const uint32_t*>(p);
     } else {
-        r.v[0] = __uint_as_float((uint32_t)*static_cast<const uint16_t*>(p) << 16);
+        r.w[0] = *static_cast<const uint16_t*>(p);
     }
 }
 template <typename T, int V>
 __device__ __forceinline__ void store_run(void* p, const Run<T, V>& r) {
     if constexpr (V == 8) {
         Chunk<T> c;
-        put(c, r.v);
+#pragma unroll
+        for (int i = 0; i < Elem<T>::kWords; ++i) c.w[i] = r.w[i];
         st_vec(p, c);
-    } else if constexpr (sizeof(typename Elem<T>::raw) == 4) {
-        *static_cast<float*>(p) = r.v[0];
+    } else if constexpr (V * sizeof(typename Elem<T>::raw) == 8) {
+        *static_cast<uint2*>(p) = make_uint2(r.w[0], r.w[1]);
+    } else if constexpr (V * sizeof(typename Elem<T>::raw) == 4) {
+        *static_cast<uint32_t*>(p) = r.w[0];
     } else {
-        *static_cast<uint16_t*>(p) = (uint16_t)pack_bf16(r.v[0], 0.f);
+        *static_cast<uint16_t*>(p) = (uint16_t)r.w[0];
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Run<T, V>& r, float (&v)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if constexpr (sizeof(typename Elem<T>::raw) == 4)
+            v[i] = __uint_as_float(r.w[i]);
+        else
+            v[i] = __uint_as_float(i & 1 ? r.w[i >> 1] & 0xFFFF0000u : r.w[i >> 1] << 16);
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void repack(Run<T, V>& r, const float (&v)[V]) {
+    if constexpr (sizeof(typename Elem<T>::raw) == 4) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) r.w[i] = __float_as_uint(v[i]);
+    } else if constexpr (V == 1) {
+        r.w[0] = pack_bf16(v[0], 0.f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) r.w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
     }
 }
 
-// 256 threads take an item each of a head of this size; 32 tokens' heads are counted in 32
-// bits.
+// 256 pairs are eight blocks of 32 lanes at most.
 constexpr int64_t kMaxHeadDim = 512, kMaxHeads = 65536;
-constexpr int kThreads = 256;
-constexpr int kAngles = 2048;  // of a block, in shared memory: 16 KB
-constexpr int kTokens = 32;    // of a block, at most
-constexpr int kAtOnce = 4;     // heads whose loads a thread issues together
+constexpr int kWarps = 8;   // of a block
+// Heads whose loads a lane issues together: with V = 8 more would cost blocks of registers.
+template <int V>
+__host__ __device__ constexpr int at_once() {
+    return V == 8 ? 2 : V == 2 ? 4 : 8;
+}
 
-// A block takes `tokens` tokens: first their angles, each once for all heads, into shared
-// memory; then every thread keeps one item of a head (V pairs: 2 V elements in two
-// runs) and goes over the heads of the tokens, `at_once` at a time.  V = 8 where
-// rot_dim / 2 and all strides are multiples of 8 elements and the pointers of 8 elements'
-// bytes; V = 1 otherwise.
+// How the warps share the work: a warp takes one token, `lanes` items of its heads (V pairs
+// each: 2 V elements in two runs) out of `blocks` times as many, and one of `parts` parts
+// of its heads, `each` heads; `across` heads at a time.  What is not turned is copied `copy`
+// elements an access.
+struct RopePlan {
+    int lanes, blocks, parts, each, across, copy;
+};
+
+// Every lane has the cosines and sines of its V pairs in registers and goes over the
+// heads with them: they are made once for all heads.  V = 8 where rot_dim / 2 and all
+// strides are multiples of 8 elements and the pointers of 8 elements' bytes; there the warp's
+// lanes make the angles of its items together, and hand them over in shared memory.
 template <typename T, int V, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, int tokens) {
+__global__ void __launch_bounds__(32 * kWarps) rope_kernel(const RopeArgs a, const RopePlan p) {
     using raw = typename Elem<T>::raw;
-    __shared__ __align__(16) float2 angle[kAngles];
-    __shared__ const raw* from[2][kTokens];
-    __shared__ raw* to[2][kTokens];
-    const int half = a.rot_dim >> 1, heads = a.heads;
-    const int64_t token0 = (int64_t)blockIdx.x * tokens;
-    const int n = (int)(a.tokens - token0 < tokens ? a.tokens - token0 : tokens);
-    for (int i = threadIdx.x; i < 2 * n; i += kThreads) {
-        const int k = i >= n, t = i - k * n;
-        const int64_t b = (token0 + t) / a.seq, s = token0 + t - b * a.seq;
-        from[k][t] = static_cast<const raw*>(a.t[k].x) + b * a.t[k].x_batch_stride +
-                     s * a.t[k].x_seq_stride;
-        to[k][t] = static_cast<raw*>(a.t[k].y) + b * a.t[k].y_batch_stride +
-                   s * a.t[k].y_seq_stride;
-    }
-    for (int i = threadIdx.x; i < n * half; i += kThreads) {
-        const int t = i / half, f = i - t * half;
-        const int64_t token = token0 + t;
-        const int64_t pos = a.positions ? a.positions[token] : a.start + token % a.seq;
-        angle[i] = cos_sin((double)pos, a.inv_freq[f], a.magnitude, a.sign);
-    }
-    __syncthreads();
+    __shared__ __align__(16) float2 angle[V == 8 ? kWarps : 1][V == 8 ? 256 : 1];
+    constexpr int kAtOnce = at_once<V>();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t token = (int64_t)blockIdx.x * kWarps + warp;
+    if (token >= a.tokens) return;
+    const int part = (int)blockIdx.y / p.blocks, block = (int)blockIdx.y - part * p.blocks;
+    const uint32_t b = (uint32_t)token / (uint32_t)a.seq, s = (uint32_t)token - b * (uint32_t)a.seq;
+    const raw* const x0 =
+        static_cast<const raw*>(a.t[0].x) + b * a.t[0].x_batch_stride + s * a.t[0].x_seq_stride;
+    const raw* const x1 =
+        static_cast<const raw*>(a.t[1].x) + b * a.t[1].x_batch_stride + s * a.t[1].x_seq_stride;
+    raw* const y0 = static_cast<raw*>(a.t[0].y) + b * a.t[0].y_batch_stride + s * a.t[0].y_seq_stride;
+    raw* const y1 = static_cast<raw*>(a.t[1].y) + b * a.t[1].y_batch_stride + s * a.t[1].y_seq_stride;
+    const int half = a.rot_dim >> 1, items = half / V;
+    const int h0 = part * p.each, h1 = min(h0 + p.each, a.heads);
+    auto in_of = [&](int h) {
+        return h < a.heads0 ? x0 + h * a.t[0].x_head_stride
+                            : x1 + (h - a.heads0) * a.t[1].x_head_stride;
+    };
+    auto out_of = [&](int h) {
+        return h < a.heads0 ? y0 + h * a.t[0].y_head_stride
+                            : y1 + (h - a.heads0) * a.t[1].y_head_stride;
+    };
 
-    // the rotated part: `items` threads a head, `rows` heads at a time
-    const int items = half / V;
     if (items > 0) {
-        const int rows = kThreads / items, row = threadIdx.x / items;
-        const int f = (threadIdx.x - row * items) * V;
+        const int sub = lane / p.lanes, own = lane - sub * p.lanes;
+        const int item = block * 32 + own, f = item * V;
+        const bool works = sub < p.across && item < items;
         const int e1 = INTERLEAVED ? 2 * f : f, e2 = INTERLEAVED ? 2 * f + V : f + half;
-        const int units = row < rows ? n * heads : 0;
-        for (int u0 = row; u0 < units; u0 += rows * kAtOnce) {
-            Run<T, V> x1[kAtOnce], x2[kAtOnce];
-            raw* y[kAtOnce];
-            const float2* cs[kAtOnce];
+        Run<T, V> r1[kAtOnce], r2[kAtOnce];
+        auto fetch = [&](int h) {
 #pragma unroll
             for (int k = 0; k < kAtOnce; ++k) {
-                const int u = u0 + k * rows;
-                y[k] = nullptr;
-                if (u < units) {
-                    const int t = u / heads, h = u - t * heads;
-                    const int w = h >= a.heads0;
-                    const int64_t hh = h - (w ? a.heads0 : 0);
-                    const raw* x = from[w][t] + hh * (w ? a.t[1] : a.t[0]).x_head_stride;
-                    y[k] = to[w][t] + hh * (w ? a.t[1] : a.t[0]).y_head_stride;
-                    cs[k] = angle + t * half + f;
-                    load_run(x1[k], x + e1);
-                    load_run(x2[k], x + e2);
+                const int hk = h + k * p.across;
+                if (works && hk < h1) {
+                    const raw* const x = in_of(hk);
+                    load_run(r1[k], x + e1);
+                    load_run(r2[k], x + e2);
                 }
             }
-#pragma unroll
-            for (int k = 0; k < kAtOnce; ++k) {
-                if (!y[k]) continue;
-                float2 turn[V];
-                if constexpr (V == 8) {
-                    const float4* const p = reinterpret_cast<const float4*>(cs[k]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 q = p[i];
-                        turn[2 * i] = make_float2(q.x, q.y);
-                        turn[2 * i + 1] = make_float2(q.z, q.w);
-                    }
-                } else {
-                    turn[0] = *cs[k];
-                }
-                if (INTERLEAVED && V > 1) {
-                    // the runs are 2 f .. 2 f + 2 V - 1: pair i is elements 2 i and 2 i + 1 of them
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float2 c = turn[i];
-                        float* const v = i < V / 2 ? x1[k].v : x2[k].v;
-                        const int e = 2 * (i % (V / 2 > 0 ? V / 2 : 1));
-                        const float p = v[e], q = v[e + 1];
-                        v[e] = p * c.x - q * c.y;
-                        v[e + 1] = q * c.x + p * c.y;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float2 c = turn[i];
-                        const float p = x1[k].v[i], q = x2[k].v[i];
-                        x1[k].v[i] = p * c.x - q * c.y;
-                        x2[k].v[i] = q * c.x + p * c.y;
-                    }
-                }
-                store_run(y[k] + e1, x1[k]);
-                store_run(y[k] + e2, x2[k]);
-            }
-        }
-    }
-    // the rest of each head, copied
-    const int rest = (a.head_dim - a.rot_dim) / V;
-    const int copies = n * heads * rest;
-    for (int i = threadIdx.x; i < copies; i += kThreads) {
-        const int u = i / rest, e = a.rot_dim + (i - u * rest) * V;
-        const int t = u / heads, h = u - t * heads;
-        const int w = h >= a.heads0;
-        const int64_t hh = h - (w ? a.heads0 : 0);
-        const raw* x = from[w][t] + hh * (w ? a.t[1] : a.t[0]).x_head_stride;
-        raw* y = to[w][t] + hh * (w ? a.t[1] : a.t[0]).y_head_stride;
-        if (x == y) continue;
+        };
+        int h = h0 + sub;
+        fetch(h);  // on its way while the angles are made
+        const double pos = (double)(a.positions ? a.positions[token] : a.start + s);
+        float2 turn[V];
         if constexpr (V == 8) {
-            Chunk<T> c;
-            ld_vec(c, x + e);
-            st_vec(y + e, c);
-        } else {
-            y[e] = x[e];
+            const int n = 8 * min(p.lanes, items - block * 32);
+            for (int i = lane; i < n; i += 32)
+                angle[warp][i] = cos_sin(pos, a.inv_freq[block * 256 + i], a.magnitude, a.sign);
+            __syncwarp();
+            const float4* const q = reinterpret_cast<const float4*>(angle[warp] + 8 * own);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 t = q[i];
+                turn[2 * i] = make_float2(t.x, t.y);
+                turn[2 * i + 1] = make_float2(t.z, t.w);
+            }
+        } else if (works) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                turn[i] = cos_sin(pos, a.inv_freq[f + i], a.magnitude, a.sign);
+        }
+        while (works && h < h1) {
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int hk = h + k * p.across;
+                if (hk >= h1) continue;
+                float u[V], v[V];
+                unpack(r1[k], u);
+                unpack(r2[k], v);
+                if (INTERLEAVED && V > 1) {
+                    // the runs are elements 2 f .. 2 f + 2 V - 1, pair i its 2 i and 2 i + 1
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        float* const w = i < V / 2 ? u : v;
+                        const int e = 2 * (i % (V > 1 ? V / 2 : 1));
+                        const float c = w[e], d = w[e + 1];
+                        w[e] = c * turn[i].x - d * turn[i].y;
+                        w[e + 1] = d * turn[i].x + c * turn[i].y;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float c = u[i], d = v[i];
+                        u[i] = c * turn[i].x - d * turn[i].y;
+                        v[i] = d * turn[i].x + c * turn[i].y;
+                    }
+                }
+                repack(r1[k], u);
+                repack(r2[k], v);
+                raw* const y = out_of(hk);
+                store_run(y + e1, r1[k]);
+                store_run(y + e2, r2[k]);
+            }
+            h += kAtOnce * p.across;
+            fetch(h);
         }
     }
+    // the rest of each head, copied by the warps of the first block of items
+    if (block > 0 || a.rot_dim == a.head_dim) return;
+    auto copy = [&](auto width) {
+        constexpr int W = decltype(width)::value, kBatch = 4;
+        const int rest = (a.head_dim - a.rot_dim) / W, n = (h1 - h0) * rest;
+        for (int i0 = lane; i0 < n; i0 += 32 * kBatch) {
+            Run<T, W> r[kBatch];
+            raw* y[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int i = i0 + 32 * k;
+                y[k] = nullptr;
+                if (i < n) {
+                    const int h = i / rest, e = a.rot_dim + (i - h * rest) * W;
+                    const raw* const x = in_of(h0 + h);
+                    y[k] = out_of(h0 + h);
+                    if (x == y[k]) {
+                        y[k] = nullptr;  // in place
+                    } else {
+                        load_run(r[k], x + e);
+                        y[k] += e;
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (y[k]) store_run(y[k], r[k]);
+        }
+    };
+    if (p.copy == 8)
+        copy(std::integral_constant<int, 8>{});
+    else if (p.copy == 2)
+        copy(std::integral_constant<int, 2>{});
+    else
+        copy(std::integral_constant<int, 1>{});
 }
 
 template <typename T, int V>
-lm_status launch_rope(const RopeArgs& a, bool interleaved, cudaStream_t s) {
+lm_status launch_rope(const RopeArgs& a, bool interleaved, int copy, cudaStream_t s) {
     const int sms = sm_count();
     if (sms <= 0) return LM_ERR_CUDA;
-    const int half = a.rot_dim >> 1;
-    // the heads that a block's threads take at once, kAtOnce times, in whole tokens; fewer
-    // where that would leave multiprocessors idle
-    const int items = half / V > 0 ? half / V : 1;
-    int64_t tokens = ((int64_t)(kThreads / items) * kAtOnce + a.heads - 1) / a.heads;
-    if (half > 0 && tokens > kAngles / half) tokens = kAngles / half;
-    if (tokens > kTokens) tokens = kTokens;
-    if (tokens > a.tokens / (2 * sms)) tokens = a.tokens / (2 * sms);
-    if (tokens < 1) tokens = 1;
-    const int64_t blocks = (a.tokens + tokens - 1) / tokens;
+    const int items = (a.rot_dim >> 1) / V;
+    RopePlan p;
+    p.copy = copy;
+    p.lanes = items < 32 ? (items > 0 ? items : 1) : 32;
+    p.blocks = items > 32 ? (items + 31) / 32 : 1;
+    p.across = 32 / p.lanes;
+    // one part, or what gives every multiprocessor 16 warps
+    const int64_t warps = a.tokens * p.blocks, want = (int64_t)sms * 16;
+    const int64_t most = (a.heads + p.across - 1) / p.across;
+    int64_t parts = warps < want ? (want + warps - 1) / warps : 1;
+    if (parts > most) parts = most;
+    p.each = (int)((a.heads + parts - 1) / parts + p.across - 1) / p.across * p.across;
+    p.parts = (a.heads + p.each - 1) / p.each;
+    // parts * blocks is at most `want` where parts > 1, and 8 otherwise: within the grid's y
+    const dim3 grid((unsigned)((a.tokens + kWarps - 1) / kWarps), (unsigned)(p.parts * p.blocks));
     timing_mark(s, 'r');
     if (interleaved)
-        rope_kernel<T, V, true><<<(unsigned)blocks, kThreads, 0, s>>>(a, (int)tokens);
+        rope_kernel<T, V, true><<<grid, 32 * kWarps, 0, s>>>(a, p);
     else
-        rope_kernel<T, V, false><<<(unsigned)blocks, kThreads, 0, s>>>(a, (int)tokens);
+        rope_kernel<T, V, false><<<grid, 32 * kWarps, 0, s>>>(a, p);
     return launch_status();
 }
 
@@ -256,8 +325,10 @@ extern "C" lm_status lm_rope(const lm_rope_tensor* tensors, int count, int64_t b
     RopeArgs a{};
     const unsigned size = dtype == LM_DTYPE_BF16 ? 2 : 4;
     const bool none = batch == 0 || seq == 0;
-    // whole chunks, of both runs of an item and of what is copied
-    bool vec = rot_dim % 16 == 0 && head_dim % 8 == 0;
+    // elements of an access: of the turned part they divide rot_dim / 2, of the copied one
+    // rot_dim and head_dim, of both the strides
+    int v = rot_dim % 16 == 0 ? 8 : rot_dim % 4 == 0 ? 2 : 1;
+    int copy = rot_dim % 8 == 0 && head_dim % 8 == 0 ? 8 : head_dim % 2 == 0 ? 2 : 1;
     for (int i = 0; i < count; ++i) {
         const lm_rope_tensor& t = tensors[i];
         if (t.heads < 0) return LM_ERR_INVALID_ARG;
@@ -275,7 +346,11 @@ extern "C" lm_status lm_rope(const lm_rope_tensor* tensors, int count, int64_t b
         const int64_t strides = (batch > 1 ? t.x_batch_stride | t.y_batch_stride : 0) |
                                 (seq > 1 ? t.x_seq_stride | t.y_seq_stride : 0) |
                                 (t.heads > 1 ? t.x_head_stride | t.y_head_stride : 0);
-        vec = vec && strides % 8 == 0 && aligned_to(t.x, 8 * size) && aligned_to(t.y, 8 * size);
+        auto fits = [&](int n) {
+            return strides % n == 0 && aligned_to(t.x, n * size) && aligned_to(t.y, n * size);
+        };
+        while (v > 1 && !fits(v)) v = v == 8 ? 2 : 1;
+        while (copy > 1 && !fits(copy)) copy = copy == 8 ? 2 : 1;
         a.t[i] = t;
         a.heads += (int)t.heads;
         if (i == 0) a.heads0 = (int)t.heads;
@@ -289,8 +364,12 @@ extern "C" lm_status lm_rope(const lm_rope_tensor* tensors, int count, int64_t b
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool il = flags & LM_ROPE_INTERLEAVED;
     if (dtype == LM_DTYPE_BF16)
-        return vec ? launch_rope<bf16_t, 8>(a, il, s) : launch_rope<bf16_t, 1>(a, il, s);
-    return vec ? launch_rope<f32_t, 8>(a, il, s) : launch_rope<f32_t, 1>(a, il, s);
+        return v == 8   ? launch_rope<bf16_t, 8>(a, il, copy, s)
+               : v == 2 ? launch_rope<bf16_t, 2>(a, il, copy, s)
+                        : launch_rope<bf16_t, 1>(a, il, copy, s);
+    return v == 8   ? launch_rope<f32_t, 8>(a, il, copy, s)
+           : v == 2 ? launch_rope<f32_t, 2>(a, il, copy, s)
+                    : launch_rope<f32_t, 1>(a, il, copy, s);
 }
 
 extern "C" lm_status lm_rope_inv_freq(double theta, int64_t rot_dim, lm_rope_scaling scaling,

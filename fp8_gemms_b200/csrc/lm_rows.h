@@ -54,9 +54,8 @@ inline lm_status dropout_args(double p, const uint64_t* rng, uint64_t offset, Dr
     d->rng = rng;
     d->offset = offset;
     const uint32_t drop = (uint32_t)lrint(p * 65536.0);
-    const uint32_t half = drop < 65535u ? drop : 65535u;
-    d->least = half << 16 | half;
-    d->live = drop < 65536u ? 0xFFFFFFFFu : 0u;
+    d->least = (drop < 65535u ? drop : 65535u) << 16;
+    d->live = drop < 65536u;
     d->scale = drop < 65536u ? (float)(65536.0 / (65536.0 - drop)) : 0.f;
     return LM_OK;
 }
