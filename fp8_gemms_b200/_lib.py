@@ -196,7 +196,10 @@ def _p(t):
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the handle alone: building a torch.cuda.Stream for it takes 3 us
+        if not torch.cuda.is_initialized():
+            torch.cuda.init()
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
@@ -398,80 +401,72 @@ def lm_fp8_lmhead_ce(X, W, labels, loss_out, dX, dW, workspace, chunk, softcap=1
 
 
 # ------------------------------------------- operators between the GEMMs
+# The checks return what the call needs (sizes, strides), so that nothing is asked of a
+# tensor twice: a small call's time is mostly this.
 _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
-
-
-def _ld(t):
-    return 0 if t is None else t.stride(0)
 
 
 def _refuse(what, why, status=1):
     raise LmError(status, f"{what}: {why}")
 
 
-def _check_rows(what, x, *others, row_vectors=()):
+def _check_rows(what, x, *others):
     """x and `others` (each may be None): [rows x cols] CUDA tensors of one type
-    and device whose columns are adjacent; `row_vectors`: [cols] ones.  Returns
-    (rows, cols, lm_dtype)."""
-    if x.dim() != 2 or not x.is_cuda:
+    and device whose columns are adjacent.  Returns (rows, cols, lm_dtype, device) and
+    the row strides (0 for None)."""
+    shape, dtype, device = x.shape, x.dtype, x.device
+    if len(shape) != 2 or not x.is_cuda:
         _refuse(what, "a 2-D CUDA tensor is wanted")
-    dtype = x.dtype
     code = _DTYPES.get(dtype)
     if code is None:
         _refuse(what, f"{dtype} is not supported", 4)
-    rows, cols = shape = x.shape
-    device = x.device
+    rows, cols = shape
+    lds = []
     for t in (x, *others):
-        if t is not None and (t.shape != shape or t.dtype != dtype or t.device != device
-                              or (cols > 1 and t.stride(1) != 1)):
+        if t is None:
+            lds.append(0)
+            continue
+        st = t.stride()
+        if (t.shape != shape or t.dtype != dtype or t.device != device
+                or (st[1] != 1 and cols > 1)):
             _refuse(what, "tensors of one shape, type and device with adjacent columns are "
                           "wanted")
-    for t in row_vectors:
-        if t is not None and (t.dim() != 1 or t.shape[0] != cols or t.dtype != dtype
-                              or t.device != device or (cols > 1 and t.stride(0) != 1)):
-            _refuse(what, f"weight and bias are [{cols}] tensors of the same type and device")
-    return rows, cols, code
+        lds.append(st[0])
+    return (rows, cols, code, device), lds
 
 
-def _check_stats(what, rows, device, *stats):
-    for t in stats:
-        if t is not None and (t.dtype != torch.float32 or t.numel() != rows or t.device != device
+def _check_vectors(what, n, dtype, device, *vectors):
+    for t in vectors:
+        if t is not None and (t.shape != (n,) or t.dtype != dtype or t.device != device
                               or not t.is_contiguous()):
-            _refuse(what, f"mean and rstd are contiguous fp32 [{rows}] tensors of the same device")
-
-
-def _check_amax(what, device, amax):
-    if amax is not None and (amax.dtype != torch.float32 or amax.numel() != 1
-                             or amax.device != device):
-        _refuse(what, "amax_out is one fp32 of the same device")
+            _refuse(what, f"a contiguous {dtype} [{n}] vector of the same device is wanted")
 
 
 def _check_rng(what, rng, offset, device):
-    if (rng.dtype not in (torch.int64, torch.uint64) or rng.numel() != 2 or rng.device != device
-            or not rng.is_contiguous()):
+    if (rng is None or rng.dtype not in (torch.int64, torch.uint64) or rng.numel() != 2
+            or rng.device != device or not rng.is_contiguous()):
         _refuse(what, "rng is a contiguous 64-bit integer {seed, offset} of the same device")
     if not 0 <= offset < 1 << 64:
         _refuse(what, "offset is an unsigned 64-bit integer")
 
 
 def _check_wgrads(what, cols, x, flags, workspace, *wgrads):
-    dtype = torch.float32 if flags & NORM_ACCUMULATE_WGRAD else x.dtype
-    for t in wgrads:
-        if t is not None and (t.dim() != 1 or t.shape[0] != cols or t.dtype != dtype
-                              or t.device != x.device or (cols > 1 and t.stride(0) != 1)):
-            _refuse(what, f"dweight and dbias are [{cols}] {dtype} tensors of the same device")
+    _check_vectors(what, cols, torch.float32 if flags & NORM_ACCUMULATE_WGRAD else x.dtype,
+                   x.device, *wgrads)
     if workspace is not None and (workspace.device != x.device or not workspace.is_contiguous()):
         _refuse(what, "the workspace is a contiguous buffer of the same device")
 
 
 def lm_layernorm_fwd(X, weight, bias, Y, mean=None, rstd=None, eps=1e-5, amax_out=None,
                      stream=None):
-    rows, cols, dt = _check_rows("lm_layernorm_fwd", X, Y, row_vectors=(weight, bias))
-    _check_stats("lm_layernorm_fwd", rows, X.device, mean, rstd)
-    _check_amax("lm_layernorm_fwd", X.device, amax_out)
-    _check(lib.lm_layernorm_fwd(_p(X), _ld(X), _p(weight), _p(bias), rows, cols, eps, dt, _p(Y),
-                                _ld(Y), _p(mean), _p(rstd), _p(amax_out), _stream(stream)),
-           "lm_layernorm_fwd")
+    what = "lm_layernorm_fwd"
+    (rows, cols, dt, device), (ldx, ldy) = _check_rows(what, X, Y)
+    _check_vectors(what, cols, X.dtype, device, weight, bias)
+    _check_vectors(what, rows, torch.float32, device, mean, rstd)
+    _check_vectors(what, 1, torch.float32, device, amax_out)
+    _check(lib.lm_layernorm_fwd(X.data_ptr(), ldx, _p(weight), _p(bias), rows, cols, eps, dt,
+                                _p(Y), ldy, _p(mean), _p(rstd), _p(amax_out), _stream(stream)),
+           what)
 
 
 def lm_layernorm_workspace_size(rows, cols):
@@ -482,53 +477,57 @@ def lm_layernorm_bwd(dY, X, weight, mean, rstd, dX, dweight, dbias, workspace, f
                      stream=None):
     """dweight, dbias: [cols] of X's type, or fp32 with NORM_ACCUMULATE_WGRAD;
     either may be None."""
-    rows, cols, dt = _check_rows("lm_layernorm_bwd", X, dY, dX, row_vectors=(weight,))
-    _check_stats("lm_layernorm_bwd", rows, X.device, mean, rstd)
-    _check_wgrads("lm_layernorm_bwd", cols, X, flags, workspace, dweight, dbias)
-    _check(lib.lm_layernorm_bwd(_p(dY), _ld(dY), _p(X), _ld(X), _p(weight), _p(mean), _p(rstd),
-                                rows, cols, dt, _p(dX), _ld(dX), _p(dweight), _p(dbias),
-                                _p(workspace), _nbytes(workspace), flags, _stream(stream)),
-           "lm_layernorm_bwd")
+    what = "lm_layernorm_bwd"
+    (rows, cols, dt, device), (ldx, lddy, lddx) = _check_rows(what, X, dY, dX)
+    _check_vectors(what, cols, X.dtype, device, weight)
+    _check_vectors(what, rows, torch.float32, device, mean, rstd)
+    _check_wgrads(what, cols, X, flags, workspace, dweight, dbias)
+    _check(lib.lm_layernorm_bwd(_p(dY), lddy, X.data_ptr(), ldx, _p(weight), _p(mean), _p(rstd),
+                                rows, cols, dt, _p(dX), lddx, _p(dweight), _p(dbias),
+                                _p(workspace), _nbytes(workspace), flags, _stream(stream)), what)
 
 
 def lm_dropout_add_fwd(X, residual, Y, p, rng, offset=0, stream=None):
-    rows, cols, dt = _check_rows("lm_dropout_add_fwd", X, residual, Y)
-    _check_rng("lm_dropout_add_fwd", rng, offset, X.device)
-    _check(lib.lm_dropout_add_fwd(_p(X), _ld(X), _p(residual), _ld(residual), rows, cols, dt, p,
-                                  _p(rng), offset, _p(Y), _ld(Y), _stream(stream)),
-           "lm_dropout_add_fwd")
+    what = "lm_dropout_add_fwd"
+    (rows, cols, dt, device), (ldx, ldr, ldy) = _check_rows(what, X, residual, Y)
+    _check_rng(what, rng, offset, device)
+    _check(lib.lm_dropout_add_fwd(X.data_ptr(), ldx, _p(residual), ldr, rows, cols, dt, p,
+                                  rng.data_ptr(), offset, _p(Y), ldy, _stream(stream)), what)
 
 
 def lm_dropout_add_bwd(dY, dX, p, rng, offset=0, stream=None):
-    rows, cols, dt = _check_rows("lm_dropout_add_bwd", dY, dX)
-    _check_rng("lm_dropout_add_bwd", rng, offset, dY.device)
-    _check(lib.lm_dropout_add_bwd(_p(dY), _ld(dY), rows, cols, dt, p, _p(rng), offset, _p(dX),
-                                  _ld(dX), _stream(stream)), "lm_dropout_add_bwd")
+    what = "lm_dropout_add_bwd"
+    (rows, cols, dt, device), (lddy, lddx) = _check_rows(what, dY, dX)
+    _check_rng(what, rng, offset, device)
+    _check(lib.lm_dropout_add_bwd(dY.data_ptr(), lddy, rows, cols, dt, p, rng.data_ptr(), offset,
+                                  _p(dX), lddx, _stream(stream)), what)
 
 
 def lm_dropout_add_layernorm_fwd(X, residual, weight, bias, S, Y, p, rng, offset=0, mean=None,
                                  rstd=None, eps=1e-5, amax_out=None, stream=None):
     what = "lm_dropout_add_layernorm_fwd"
-    rows, cols, dt = _check_rows(what, X, residual, S, Y, row_vectors=(weight, bias))
-    _check_stats(what, rows, X.device, mean, rstd)
-    _check_amax(what, X.device, amax_out)
-    _check_rng(what, rng, offset, X.device)
+    (rows, cols, dt, device), (ldx, ldr, lds, ldy) = _check_rows(what, X, residual, S, Y)
+    _check_vectors(what, cols, X.dtype, device, weight, bias)
+    _check_vectors(what, rows, torch.float32, device, mean, rstd)
+    _check_vectors(what, 1, torch.float32, device, amax_out)
+    _check_rng(what, rng, offset, device)
     _check(lib.lm_dropout_add_layernorm_fwd(
-        _p(X), _ld(X), _p(residual), _ld(residual), _p(weight), _p(bias), rows, cols, eps, dt, p,
-        _p(rng), offset, _p(S), _ld(S), _p(Y), _ld(Y), _p(mean), _p(rstd), _p(amax_out),
+        X.data_ptr(), ldx, _p(residual), ldr, _p(weight), _p(bias), rows, cols, eps, dt, p,
+        rng.data_ptr(), offset, _p(S), lds, _p(Y), ldy, _p(mean), _p(rstd), _p(amax_out),
         _stream(stream)), what)
 
 
 def lm_dropout_add_layernorm_bwd(dY, dS, S, weight, mean, rstd, p, rng, dX, dR, dweight, dbias,
                                  workspace, offset=0, flags=0, stream=None):
     what = "lm_dropout_add_layernorm_bwd"
-    rows, cols, dt = _check_rows(what, S, dY, dS, dX, dR, row_vectors=(weight,))
-    _check_stats(what, rows, S.device, mean, rstd)
-    _check_rng(what, rng, offset, S.device)
+    (rows, cols, dt, device), (lds, lddy, ldds, lddx, lddr) = _check_rows(what, S, dY, dS, dX, dR)
+    _check_vectors(what, cols, S.dtype, device, weight)
+    _check_vectors(what, rows, torch.float32, device, mean, rstd)
+    _check_rng(what, rng, offset, device)
     _check_wgrads(what, cols, S, flags, workspace, dweight, dbias)
     _check(lib.lm_dropout_add_layernorm_bwd(
-        _p(dY), _ld(dY), _p(dS), _ld(dS), _p(S), _ld(S), _p(weight), _p(mean), _p(rstd), rows,
-        cols, dt, p, _p(rng), offset, _p(dX), _ld(dX), _p(dR), _ld(dR), _p(dweight), _p(dbias),
+        _p(dY), lddy, _p(dS), ldds, S.data_ptr(), lds, _p(weight), _p(mean), _p(rstd), rows, cols,
+        dt, p, rng.data_ptr(), offset, _p(dX), lddx, _p(dR), lddr, _p(dweight), _p(dbias),
         _p(workspace), _nbytes(workspace), flags, _stream(stream)), what)
 
 
@@ -552,19 +551,19 @@ def lm_rope(xs, ys, inv_freq, positions=None, start=0, magnitude=1.0, flags=0, s
         _refuse("lm_rope", "positions is a contiguous int64 [batch, seq] of the same device")
     if not -1 << 63 <= start < 1 << 63:
         _refuse("lm_rope", "start is a signed 64-bit integer")
-    arr = (RopeTensor * len(xs))()
-    for t, x, y in zip(arr, xs, ys):
-        if (x.shape != y.shape or x.dim() != 4 or x.shape[0] != batch or x.shape[1] != seq
-                or x.shape[3] != head_dim or x.dtype != dtype or y.dtype != dtype
+    parts = []
+    for x, y in zip(xs, ys):
+        shape, sx, sy = x.shape, x.stride(), y.stride()
+        if (len(shape) != 4 or y.shape != shape or shape[0] != batch or shape[1] != seq
+                or shape[3] != head_dim or x.dtype != dtype or y.dtype != dtype
                 or x.device != device or y.device != device
-                or (head_dim > 1 and (x.stride(3) != 1 or y.stride(3) != 1))):
+                or (head_dim > 1 and (sx[3] != 1 or sy[3] != 1))):
             _refuse("lm_rope", "tensors of one type, device, batch, seq and head_dim with adjacent "
                                "elements are wanted")
-        t.x, t.y, t.heads = x.data_ptr(), y.data_ptr(), x.shape[2]
-        t.x_batch_stride, t.x_seq_stride, t.x_head_stride, _ = x.stride()
-        t.y_batch_stride, t.y_seq_stride, t.y_head_stride, _ = y.stride()
-    _check(lib.lm_rope(arr, len(xs), batch, seq, head_dim, 2 * inv_freq.shape[0], code,
-                       _p(inv_freq), _p(positions), start, magnitude, flags, _stream(stream)),
+        parts.append(RopeTensor(x.data_ptr(), y.data_ptr(), shape[2], *sx[:3], *sy[:3]))
+    arr = (RopeTensor * len(parts))(*parts)
+    _check(lib.lm_rope(arr, len(parts), batch, seq, head_dim, 2 * inv_freq.shape[0], code,
+                       inv_freq.data_ptr(), _p(positions), start, magnitude, flags, _stream(stream)),
            "lm_rope")
 
 

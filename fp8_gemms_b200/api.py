@@ -365,10 +365,10 @@ def _placed(fn):
     allocated too."""
     @functools.wraps(fn)
     def placed(x, *args, stream=None, **kw):
-        device = (x[0] if isinstance(x, (list, tuple)) else x).device
-        if device.type != "cuda" or (stream is None
-                                     and device.index == torch.cuda.current_device()):
-            return fn(x, *args, **kw)
+        t = x[0] if isinstance(x, (list, tuple)) else x
+        if not t.is_cuda or (stream is None and t.get_device() == torch._C._cuda_getDevice()):
+            return fn(x, *args, **kw)  # a host tensor is refused by the call itself
+        device = t.device
         with torch.cuda.device(device):
             with torch.cuda.stream(stream or torch.cuda.current_stream(device)):
                 return fn(x, *args, **kw)
@@ -376,20 +376,23 @@ def _placed(fn):
 
 
 def _stats(x):
-    both = torch.empty(2, x.shape[0], dtype=torch.float32, device=x.device)
-    return both[0], both[1]
+    if x.dim() != 2:
+        _lib._refuse("the rows' statistics", "a 2-D CUDA tensor is wanted")
+    mean = x.new_empty(x.shape[0], dtype=torch.float32)
+    return mean, torch.empty_like(mean)
 
 
 def _wgrads(x, dweight, dbias, accumulate):
     """dweight, dbias and the workspace of a norm's backward."""
+    if x.dim() != 2:
+        _lib._refuse("the weight gradients", "a 2-D CUDA tensor is wanted")
     rows, cols = x.shape
     if not accumulate:
         if dweight is None:
-            dweight = torch.empty(cols, dtype=x.dtype, device=x.device)
+            dweight = x.new_empty(cols)
         if dbias is None:
-            dbias = torch.empty(cols, dtype=x.dtype, device=x.device)
-    ws = torch.empty(_lib.lm_layernorm_workspace_size(rows, cols), dtype=torch.uint8,
-                     device=x.device)
+            dbias = torch.empty_like(dweight)
+    ws = x.new_empty(_lib.lib.lm_layernorm_workspace_size(rows, cols), dtype=torch.uint8)
     return dweight, dbias, ws
 
 

@@ -287,7 +287,8 @@ __global__ void __launch_bounds__(fwd_bound<T, VEC, WARPS>(), fwd_blocks<T, VEC,
     const void* const x = row_at<T>(a.x, row, a.ldx);
     Chunk<T> c[NCH];
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) c[i] = load_chunk<T, VEC, FULL>(x, first + i * kWarpCols, lane, cols);
+    for (int i = 0; i < NCH; ++i)
+        c[i] = load_chunk<T, VEC, FULL>(x, first + i * kWarpCols, lane, cols);
     if (DROP) {
         const void* const residual = row_at<T>(a.residual, row, a.ldr);
         void* const s = row_at<T>(a.s, row, a.lds);
@@ -307,9 +308,9 @@ __global__ void __launch_bounds__(fwd_bound<T, VEC, WARPS>(), fwd_blocks<T, VEC,
         }
     }
     float mean, sq;
-    warp_moments<VEC, FULL>(c, first, lane, cols,
-                            FULL || (!ONE && warp < warps - 1) ? 1.0 / (NCH * kWarpCols) : a.inv_last,
-                            mean, sq);
+    const bool whole = FULL || (!ONE && warp < warps - 1);
+    const double inv_own = whole ? 1.0 / (NCH * kWarpCols) : a.inv_last;
+    warp_moments<VEC, FULL>(c, first, lane, cols, inv_own, mean, sq);
     row_moments(lane, warp, ONE ? 1 : warps, buf, cols, NCH * kWarpCols, a.inv_cols, mean, sq,
                 [] { __syncthreads(); });
     const float rstd = rsqrtf(sq * (float)a.inv_cols + a.eps);
@@ -386,21 +387,19 @@ __device__ __forceinline__ void group_sum2(const Group& g, float* buf, float& a,
     b = upper ? v : other;
 }
 
-// Threads of a backward block, at most: what the registers of its sums leave room for.
-template <typename T, int NCH>
-__host__ __device__ constexpr int bwd_threads() {
-    return 512;
-}
+// Threads of a backward block, at most: 128 registers each, of which the sums take up to
+// 64.
+constexpr int kBwdThreads = 512;
 
 // The backward pass, every tensor read once for dx and the weight gradients.  A thread
 // keeps its NCH chunks' sums over its rows in registers; at the end the block adds its
 // groups' sums and writes one part of the partial sums.  With four chunks a thread the
 // sums leave no registers for the row and the weight: they are read from shared
 // memory again for the second sweep.
-// VEC: rows come by asynchronous copies, `stages` - 1 ahead; otherwise by scalar loads, one
-// at a time.
+// VEC: rows come by asynchronous copies, `stages` - 1 ahead; otherwise by scalar loads into
+// registers, one ahead (ds, for which there are none, as it is used).
 template <typename T, bool VEC, int NCH, bool DROP, bool FULL>
-__global__ void __launch_bounds__(bwd_threads<T, NCH>(), 1)
+__global__ void __launch_bounds__(kBwdThreads, 1)
     norm_bwd_kernel(const BwdArgs a, int warps, int stages, float* part) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float buf[2 * 64];
@@ -439,6 +438,7 @@ __global__ void __launch_bounds__(bwd_threads<T, NCH>(), 1)
     const char* ds = static_cast<const char*>(a.ds) + (has_ds ? row * a.ldds * kSize + from0 : 0);
     char* dres = static_cast<char*>(a.dres) + row * a.lddr * kSize + at0;
     char* dx = static_cast<char*>(a.dx) + (DROP ? row * a.lddx * kSize + at0 : 0);
+    Chunk<T> next_d[VEC ? 1 : NCH], next_c[VEC ? 1 : NCH];
     auto fetch = [&](uint32_t r, uint32_t to) {
         if (r < rows) {
 #pragma unroll
@@ -451,13 +451,8 @@ __global__ void __launch_bounds__(bwd_threads<T, NCH>(), 1)
                     slots.fill(to, NCH + i, s + i * kNext, h1, h2);
                     if (has_ds) slots.fill(to, 2 * NCH + i, ds + i * kNext, h1, h2);
                 } else {
-                    slots.put(to, i,
-                              load_chunk<T, VEC>(row_at<T>(a.dy, r, a.lddy), base, g.lane, cols));
-                    slots.put(to, NCH + i,
-                              load_chunk<T, VEC>(row_at<T>(a.s, r, a.lds), base, g.lane, cols));
-                    if (has_ds)
-                        slots.put(to, 2 * NCH + i, load_chunk<T, VEC>(row_at<T>(a.ds, r, a.ldds),
-                                                                      base, g.lane, cols));
+                    next_d[i] = load_chunk<T, VEC>(row_at<T>(a.dy, r, a.lddy), base, g.lane, cols);
+                    next_c[i] = load_chunk<T, VEC>(row_at<T>(a.s, r, a.lds), base, g.lane, cols);
                 }
             }
         }
@@ -476,6 +471,8 @@ __global__ void __launch_bounds__(bwd_threads<T, NCH>(), 1)
                 if (!chunk_has<true, FULL>(first + i * kWarpCols, g.lane, cols))
                     slots.put(0, k * NCH + i, Chunk<T>{});
         for (int k = 0; k < stages - 1; ++k) fetch(row + k * row_step, k * kRow);
+    } else {
+        fetch(row, 0);
     }
     // lane l has the mean of the group's row l of 16, lane 16 + l its rstd; `next_stats`: of
     // the 16 rows after them
@@ -488,17 +485,24 @@ __global__ void __launch_bounds__(bwd_threads<T, NCH>(), 1)
     // the kernel that adds the parts may come and wait
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __syncthreads();  // the weight
-    uint32_t at = 0, ahead = (stages - 1) * kRow;  // bytes to this row's slots, and to the free ones
+    // bytes to this row's slots, and to the free ones
+    uint32_t at = 0, ahead = (stages - 1) * kRow;
     int mine = 2 * warps * g.group;  // this group's part of one buffer or the other
     for (uint32_t k = 0; row < rows; ++k, row += row_step) {
         if (k % 16 == 0) {
             stats = next_stats;
             fetch_stats((uint64_t)row + 16ull * row_step);
         }
-        if (Slots<T>::kWide) __syncwarp();  // all have read what is overwritten now
-        fetch(row + (stages - 1) * row_step, ahead);
-        if (VEC) copies_wait(stages - 1);
-        if (Slots<T>::kWide) __syncwarp();  // the others' copies
+        if (VEC && Slots<T>::kWide) __syncwarp();  // all have read what is overwritten now
+        if (VEC) {
+            fetch(row + (stages - 1) * row_step, ahead);
+            copies_wait(stages - 1);
+            if (Slots<T>::kWide) __syncwarp();  // the others' copies
+        } else {
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) d[i] = next_d[i], c[i] = next_c[i];
+            fetch(row + row_step, 0);
+        }
         const float mean = __shfl_sync(0xFFFFFFFFu, stats, k % 16);
         const float rstd = __shfl_sync(0xFFFFFFFFu, stats, 16 + k % 16);
         const F2 minus_mean = make_f2(-mean, -mean), r2 = make_f2(rstd, rstd);
@@ -506,7 +510,7 @@ __global__ void __launch_bounds__(bwd_threads<T, NCH>(), 1)
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
             if (NCH > 2 && i == 2) __syncwarp();  // or the compiler loads all four, and spills
-            d[i] = slots.take(at, i), c[i] = slots.take(at, NCH + i);
+            if (VEC) d[i] = slots.take(at, i), c[i] = slots.take(at, NCH + i);
             if (kAgain) w[i] = ws.take(0, i);
 #pragma unroll
             for (int j = 0; j < kPairs; ++j) {
@@ -536,7 +540,9 @@ __global__ void __launch_bounds__(bwd_threads<T, NCH>(), 1)
                 w[i] = ws.take(0, i);
             }
             Chunk<T> up, out;
-            if (has_ds) up = slots.take(at, 2 * NCH + i);
+            if (has_ds)
+                up = VEC ? slots.take(at, 2 * NCH + i)
+                         : load_chunk<T, VEC>(row_at<T>(a.ds, row, a.ldds), base, g.lane, cols);
             F2 v[kPairs];
 #pragma unroll
             for (int j = 0; j < kPairs; ++j) {
@@ -554,7 +560,8 @@ __global__ void __launch_bounds__(bwd_threads<T, NCH>(), 1)
                 const Keep<VEC> keep = keep_of<VEC>(renewed(key), a.drop, row, base, g.lane);
                 const F2 scale = make_f2(a.drop.scale, a.drop.scale);
 #pragma unroll
-                for (int j = 0; j < kPairs; ++j) put2(out, j, kept(mul2(v[j], scale), keep, a.drop, j));
+                for (int j = 0; j < kPairs; ++j)
+                    put2(out, j, kept(mul2(v[j], scale), keep, a.drop, j));
                 if (VEC) {
                     if (chunk_has<true, FULL>(base, g.lane, cols)) st_vec(dx + i * kNext, out);
                 } else {
@@ -736,8 +743,8 @@ __global__ void __launch_bounds__(256) norm_bwd_wide_kernel(const BwdArgs a) {
             const Keep<VEC> keep = keep_of<VEC>(key, a.drop, (uint32_t)row, base, lane);
 #pragma unroll
             for (int j = 0; j < kPairs; ++j)
-                put2(out, j, kept(make_f2(v[2 * j] * a.drop.scale, v[2 * j + 1] * a.drop.scale), keep,
-                                  a.drop, j));
+                put2(out, j, kept(mul2(make_f2(v[2 * j], v[2 * j + 1]),
+                                       make_f2(a.drop.scale, a.drop.scale)), keep, a.drop, j));
             store_chunk<T, VEC>(row_at<T>(a.dx, row, a.lddx), base, lane, cols, out);
         }
     }
@@ -752,7 +759,8 @@ __global__ void __launch_bounds__(256) norm_wgrad_kernel(const BwdArgs a, float*
     const int cols = (int)a.cols;
     const int base = (int)blockIdx.x * kWarpCols;
     float dw[kChunk] = {}, db[kChunk] = {};
-    for (int64_t row = (int64_t)blockIdx.y * 8 + warp; row < a.rows; row += (int64_t)gridDim.y * 8) {
+    const int64_t step = (int64_t)gridDim.y * 8;
+    for (int64_t row = (int64_t)blockIdx.y * 8 + warp; row < a.rows; row += step) {
         const Chunk<T> d = load_chunk<T, VEC>(row_at<T>(a.dy, row, a.lddy), base, lane, cols);
         const Chunk<T> c = load_chunk<T, VEC>(row_at<T>(a.s, row, a.lds), base, lane, cols);
         const float mean = a.mean[row], rstd = a.rstd[row];
@@ -784,8 +792,8 @@ __global__ void __launch_bounds__(256) norm_wgrad_kernel(const BwdArgs a, float*
 // each, at most ten loads in flight at once.  It may be launched before the kernel that
 // writes the parts has ended, and waits for that.
 template <typename T, bool ACCUM>
-__global__ void __launch_bounds__(1024) norm_wgrad_sum_kernel(const float* part, int parts, int cols,
-                                                              void* dweight, void* dbias) {
+__global__ void __launch_bounds__(1024)
+    norm_wgrad_sum_kernel(const float* part, int parts, int cols, void* dweight, void* dbias) {
     __shared__ float sum[32][33];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     void* out = blockIdx.y ? dbias : dweight;
@@ -831,10 +839,9 @@ lm_status sum_parts(const float* part, int parts, int64_t cols, void* dweight, v
     config.attrs = &early;
     config.numAttrs = 1;
     timing_mark(s, 'n');
-    if (cudaLaunchKernelEx(&config, norm_wgrad_sum_kernel<T, ACCUM>, part, parts, (int)cols, dweight,
-                           dbias) != cudaSuccess)
-        return LM_ERR_CUDA;
-    return launch_status();
+    const cudaError_t e = cudaLaunchKernelEx(&config, norm_wgrad_sum_kernel<T, ACCUM>, part, parts,
+                                             (int)cols, dweight, dbias);
+    return e == cudaSuccess ? launch_status() : LM_ERR_CUDA;
 }
 
 template <typename T, bool VEC, int NCH, int WARPS, bool ONE, bool DROP>
@@ -917,8 +924,7 @@ lm_status launch_fwd(const FwdArgs& a, cudaStream_t s) {
 template <typename T, bool VEC, int NCH, bool DROP>
 bool run_bwd(const BwdArgs& a, int64_t wc, int sms, float* part, cudaStream_t s, int* parts) {
     const int warps = (int)((wc + NCH - 1) / NCH), chunk = warps * NCH * Slots<T>::kBytes;
-    Plan p = plan(a.rows, warps, bwd_threads<T, NCH>(), sms, chunk, (DROP ? 3 : 2) * chunk,
-                  VEC ? 3 : 1, VEC ? 2 : 1);
+    Plan p = plan(a.rows, warps, kBwdThreads, sms, chunk, VEC ? (DROP ? 3 : 2) * chunk : 0, 3, 2);
     if (p.groups == 0) return false;
     const int sums = p.groups > 1 ? 32 * warps * NCH * kChunk * 2 * (int)sizeof(float) : 0;
     if (p.bytes < sums) p.bytes = sums;
@@ -939,14 +945,18 @@ lm_status launch_bwd(const BwdArgs& a, void* dweight, void* dbias, bool accum, f
     const int sms = sm_count();
     if (sms <= 0 && a.rows > 0) return LM_ERR_CUDA;
     const bool wgrad = dweight || dbias;
-    constexpr int kNch = VEC && sizeof(typename Elem<T>::raw) == 2 ? 4 : 2;
+    // Chunks a thread: two up to 4096 columns (two groups of eight warps a block), four beyond
+    // for bf16 (12288: 178 us with 16384 rows, two chunks and 24 warps 190); one where two
+    // would spill
+    constexpr bool bf16 = sizeof(typename Elem<T>::raw) == 2;
+    constexpr int kTwo = !VEC && DROP && !bf16 ? 1 : 2, kNch = VEC && bf16 ? 4 : kTwo;
     const int64_t wc = (a.cols + kWarpCols - 1) / kWarpCols;
     int parts = 0;
     if (a.rows > 0) {
         float* const p = wgrad ? part : nullptr;
         timing_mark(s, 'n');
         if (wc == 1    ? run_bwd<T, VEC, 1, DROP>(a, wc, sms, p, s, &parts)
-            : wc <= 16 ? run_bwd<T, VEC, 2, DROP>(a, wc, sms, p, s, &parts)
+            : wc <= 16 ? run_bwd<T, VEC, kTwo, DROP>(a, wc, sms, p, s, &parts)
                        : wc <= 16 * kNch && run_bwd<T, VEC, kNch, DROP>(a, wc, sms, p, s, &parts)) {
             if (parts == 0) return LM_ERR_CUDA;
         } else {

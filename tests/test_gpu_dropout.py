@@ -15,6 +15,10 @@ SEED, OFFSET = 0x9E3779B97F4A7C15, 0xFFFFFFFFFFFFFFF0   # the offset wraps with 
 SHAPES = [(1, 1, BF, 0, 0), (7, 3, F32, 0, 0), (33, 8, BF, 0, 0), (5, 24, F32, 8, 8),
           (64, 257, BF, 3, 1), (40, 1000, BF, 0, 0), (129, 1001, BF, 0, 0), (16, 2056, F32, 0, 0),
           (21, 4096, BF, 0, 0), (3, 12288, BF, 8, 8), (2, 40001, F32, 0, 0), (2000, 16, BF, 0, 0)]
+# whole tiles of four (bf16) and two (fp32) times 256 columns; rows of 3, 9 and 16 groups
+# of eight, several to a warp
+SHAPES += [(301, 1024, BF, 0, 0), (300, 512, F32, 8, 8), (77, 3000, BF, 0, 0), (1001, 24, BF, 0, 0),
+           (333, 72, F32, 0, 0), (129, 128, BF, 8, 0), (65, 136, BF, 0, 0)]
 IDS = [f"{r}x{c}-{'bf16' if d is BF else 'fp32'}-{p}-{s}" for r, c, d, p, s in SHAPES]
 
 
@@ -147,7 +151,11 @@ def test_mask_past_two_to_the_31_elements():
 
 # ------------------------------------------------- fused with the layer norm
 FUSED = SHAPES + [(150, 1032, BF, 0, 0), (300, 520, BF, 0, 0), (6, 8191, BF, 0, 0),
-                  (3, 32768, BF, 0, 0), (2, 33000, F32, 0, 0), (5, 8192, BF, 0, 0)]
+                  (3, 32768, BF, 0, 0), (2, 33000, F32, 0, 0), (5, 8192, BF, 0, 0),
+                  (5001, 256, F32, 0, 0), (2601, 512, BF, 0, 0), (1301, 1000, F32, 0, 0),
+                  (1301, 1001, BF, 0, 0), (701, 2048, BF, 8, 8), (701, 2049, F32, 0, 0),
+                  (331, 4096, F32, 0, 0), (311, 5120, BF, 0, 0), (201, 8192, BF, 0, 0),
+                  (181, 8191, BF, 0, 0), (151, 12296, BF, 0, 0), (101, 16384, BF, 0, 0)]
 FUSED_IDS = [f"{r}x{c}-{'bf16' if d is BF else 'fp32'}-{p}-{s}" for r, c, d, p, s in FUSED]
 
 

@@ -17,6 +17,16 @@ SHAPES = [(1, 1, BF, 0, 0), (3, 1, F32, 2, 1), (5, 7, BF, 0, 0), (2, 8, BF, 0, 0
           (301, 2048, BF, 0, 0), (19, 4096, BF, 0, 8), (5, 4104, F32, 0, 0), (6, 8191, BF, 0, 0),
           (4, 12288, BF, 0, 0), (3, 16384, F32, 0, 0), (2, 20001, BF, 0, 0), (3, 32768, BF, 0, 0),
           (2, 33000, F32, 0, 0), (2, 40008, BF, 8, 0), (1, 70001, F32, 0, 0)]
+# many rows: the forward's kernels for a row a warp and a row a block, with and without
+# whole warps of columns, and the backward's groups, each at its first and last widths
+SHAPES += [(5001, 256, BF, 0, 0), (5001, 248, F32, 0, 0), (2601, 512, BF, 0, 0),
+           (2601, 504, F32, 0, 0), (1301, 1024, BF, 0, 0), (1301, 1024, F32, 0, 0),
+           (1301, 1000, BF, 0, 0), (1301, 1001, BF, 0, 0), (1001, 1032, F32, 0, 0),
+           (701, 2048, BF, 8, 8), (701, 2056, BF, 0, 0), (701, 2049, F32, 0, 0),
+           (331, 4096, F32, 0, 0), (331, 4104, BF, 0, 0), (311, 5120, BF, 0, 0),
+           (201, 8192, BF, 0, 0), (181, 8191, F32, 0, 0), (151, 12288, BF, 0, 0),
+           (121, 12296, BF, 0, 0), (101, 16384, BF, 0, 0), (99, 16385, BF, 0, 0),
+           (61, 32768, F32, 0, 0), (61, 32760, BF, 0, 0)]
 IDS = [f"{r}x{c}-{'bf16' if d is BF else 'fp32'}-{p}-{s}" for r, c, d, p, s in SHAPES]
 
 

@@ -202,6 +202,8 @@ def test_python_calls_refuse_what_they_cannot_run(L):
     freq = torch.ones(8, dtype=torch.float64)
     for call in [lambda: api.layernorm(x), lambda: api.layernorm(x[0]),
                  lambda: api.layernorm_backward(x, x, None, x[:, 0].float(), x[:, 0].float()),
+                 lambda: api.layernorm_backward(x[0], x[0], None, x[0].float(), x[0].float()),
+                 lambda: api.layernorm(x[0, 0]),
                  lambda: api.dropout_add(x, 0.1, rng), lambda: api.dropout_add_backward(x, 0.1, rng),
                  lambda: api.dropout_add_layernorm(x, x, None, None, 0.1, rng),
                  lambda: api.dropout_add_layernorm_backward(x, None, x, None, x[:, 0].float(),
