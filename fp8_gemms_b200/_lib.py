@@ -412,39 +412,42 @@ def _refuse(what, why, status=1):
 
 def _check_rows(what, x, *others):
     """x and `others` (each may be None): [rows x cols] CUDA tensors of one type
-    and device whose columns are adjacent.  Returns (rows, cols, lm_dtype, device) and
-    the row strides (0 for None)."""
-    shape, dtype, device = x.shape, x.dtype, x.device
-    if len(shape) != 2 or not x.is_cuda:
+    and device whose columns are adjacent.  Returns (rows, cols, lm_dtype, device index)
+    and the row strides (0 for None)."""
+    shape, dtype, device = x.shape, x.dtype, x.get_device()
+    if len(shape) != 2 or device < 0:
         _refuse(what, "a 2-D CUDA tensor is wanted")
     code = _DTYPES.get(dtype)
     if code is None:
         _refuse(what, f"{dtype} is not supported", 4)
     rows, cols = shape
-    lds = []
-    for t in (x, *others):
+    ld, step = x.stride()
+    if step != 1 and cols > 1:
+        _refuse(what, "adjacent columns are wanted")
+    lds = [ld]
+    for t in others:
         if t is None:
             lds.append(0)
             continue
-        st = t.stride()
-        if (t.shape != shape or t.dtype != dtype or t.device != device
-                or (st[1] != 1 and cols > 1)):
-            _refuse(what, "tensors of one shape, type and device with adjacent columns are "
-                          "wanted")
-        lds.append(st[0])
+        if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+            _refuse(what, "tensors of one shape, type and device are wanted")
+        ld, step = t.stride()
+        if step != 1 and cols > 1:
+            _refuse(what, "adjacent columns are wanted")
+        lds.append(ld)
     return (rows, cols, code, device), lds
 
 
 def _check_vectors(what, n, dtype, device, *vectors):
     for t in vectors:
-        if t is not None and (t.shape != (n,) or t.dtype != dtype or t.device != device
-                              or not t.is_contiguous()):
+        if t is not None and (t.shape != (n,) or t.dtype is not dtype
+                              or t.get_device() != device or not t.is_contiguous()):
             _refuse(what, f"a contiguous {dtype} [{n}] vector of the same device is wanted")
 
 
 def _check_rng(what, rng, offset, device):
     if (rng is None or rng.dtype not in (torch.int64, torch.uint64) or rng.numel() != 2
-            or rng.device != device or not rng.is_contiguous()):
+            or rng.get_device() != device or not rng.is_contiguous()):
         _refuse(what, "rng is a contiguous 64-bit integer {seed, offset} of the same device")
     if not 0 <= offset < 1 << 64:
         _refuse(what, "offset is an unsigned 64-bit integer")
@@ -452,8 +455,8 @@ def _check_rng(what, rng, offset, device):
 
 def _check_wgrads(what, cols, x, flags, workspace, *wgrads):
     _check_vectors(what, cols, torch.float32 if flags & NORM_ACCUMULATE_WGRAD else x.dtype,
-                   x.device, *wgrads)
-    if workspace is not None and (workspace.device != x.device or not workspace.is_contiguous()):
+                   x.get_device(), *wgrads)
+    if workspace is not None and (workspace.get_device() != x.get_device() or not workspace.is_contiguous()):
         _refuse(what, "the workspace is a contiguous buffer of the same device")
 
 
@@ -538,14 +541,14 @@ def lm_rope(xs, ys, inv_freq, positions=None, start=0, magnitude=1.0, flags=0, s
     if not 1 <= len(xs) <= 2 or len(ys) != len(xs) or xs[0].dim() != 4 or not xs[0].is_cuda:
         _refuse("lm_rope", "one or two 4-D CUDA tensors and as many outputs are wanted")
     batch, seq, _, head_dim = xs[0].shape
-    dtype, device = xs[0].dtype, xs[0].device
+    dtype, device = xs[0].dtype, xs[0].get_device()
     code = _DTYPES.get(dtype)
     if code is None:
         _refuse("lm_rope", f"{dtype} is not supported", 4)
-    if (inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or inv_freq.device != device
+    if (inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or inv_freq.get_device() != device
             or not inv_freq.is_contiguous()):
         _refuse("lm_rope", "inv_freq is a contiguous fp64 vector of the same device")
-    if positions is not None and (positions.dtype != torch.int64 or positions.device != device
+    if positions is not None and (positions.dtype != torch.int64 or positions.get_device() != device
                                   or positions.numel() != batch * seq
                                   or not positions.is_contiguous()):
         _refuse("lm_rope", "positions is a contiguous int64 [batch, seq] of the same device")
@@ -555,8 +558,8 @@ def lm_rope(xs, ys, inv_freq, positions=None, start=0, magnitude=1.0, flags=0, s
     for x, y in zip(xs, ys):
         shape, sx, sy = x.shape, x.stride(), y.stride()
         if (len(shape) != 4 or y.shape != shape or shape[0] != batch or shape[1] != seq
-                or shape[3] != head_dim or x.dtype != dtype or y.dtype != dtype
-                or x.device != device or y.device != device
+                or shape[3] != head_dim or x.dtype is not dtype or y.dtype is not dtype
+                or x.get_device() != device or y.get_device() != device
                 or (head_dim > 1 and (sx[3] != 1 or sy[3] != 1))):
             _refuse("lm_rope", "tensors of one type, device, batch, seq and head_dim with adjacent "
                                "elements are wanted")

@@ -8,10 +8,23 @@
 //   g = dy w;  ds' = r (g - mean(g) - h mean(g h));  dw = sum dy h;  db = sum dy
 //   dresidual = ds + ds';  dx = dropout(dresidual), the forward's mask made again
 //
-// All sums are fp32; the variance is that of the centred values (a second sweep),
-// so a large mean costs no digits.  The norm's backward sums over the rows
+// All sums are fp32; the variance is that of the centred values, so a large mean costs
+// no digits.  The only roundings to fewer bits are those of bf16 outputs, once
+// each, and of s, which the norm is defined on.  The norm's backward sums over the rows
 // go through per-block partial sums in the workspace and a second kernel, in a
 // fixed order: no atomics, the same bits from call to call.
+//
+// Bound by HBM: every tensor read and written once, 4 bytes an element of a bf16
+// forward, 6 of a backward, 8 and 10 fused with dropout.  What has to be kept
+// small for that is the number of instructions (an SM gets 23 bytes a clock: 5.7 elements of
+// the forward), hence the packed fp32 pairs, one exchange of sums a row, addresses with
+// constant offsets and kernels without tests for whole rows.  One B200, kernels back to
+// back for some ms, of the 6.46 TB/s that a copy reaches (in brackets):
+//   forward        16384 x 4096 bf16 42.5 us (98%), 8192 x 8192 fp32 81 us (102%)
+//   backward       16384 x 4096 bf16 65 us (96%), of which the sum of the parts 4
+//   fused forward  8192 x 5120 bf16 52.5 us (99%); fused backward 8192 x 8192 108 (96%)
+// Over longer times the 1 kW limit lowers the SM clock to 1.6-1.8 GHz and all take 3-12%
+// longer, the copy 3%.
 #include <type_traits>
 
 #include "lm_chunk.cuh"
@@ -140,6 +153,9 @@ __device__ __forceinline__ void group_barrier(int id, int threads) {
 }
 
 constexpr int kSmemBytes = 226 * 1024;  // dynamic shared memory of a block, at most
+// Rows are held two ahead of use where they fit this, else one: beyond it too little of the
+// SM's 256 KB is left as cache (16384 x 5120 bf16, 86 us with 130 KB and 92 with 190).
+constexpr int kManyBytes = 160 * 1024;
 
 // Mean and sum of centred squares of a row from its warps' own: with n_w columns, sum s_w
 // and centred squares q_w in warp w, the row has mean m = sum s_w / n and centred
@@ -274,7 +290,7 @@ __host__ __device__ constexpr int fwd_bound() {
 // The row in registers, read once: its warps (blockDim / 32 of them, or with ONE
 // one, and blockDim / 32 rows a block) take NCH x 256 columns each.
 // FULL: VEC, a multiple of NCH x 256 columns, a weight and a bias, so that nothing is
-// tested for each access: a third of the instructions of a bf16 row.
+// tested for each access: 27% fewer instructions for a bf16 row.
 // WARPS: the most a block has.
 template <typename T, bool VEC, int NCH, int WARPS, bool ONE, bool DROP, bool FULL>
 __global__ void __launch_bounds__(fwd_bound<T, VEC, WARPS>(), fwd_blocks<T, VEC, WARPS>())
@@ -630,7 +646,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 }
 
 // One block a row, the row read again for each sweep: for rows that do not fit
-// a block's registers.
+// a block's registers (beyond the widths in launch_fwd and launch_bwd).
 template <typename T, bool VEC, bool DROP>
 __global__ void __launch_bounds__(256) norm_fwd_wide_kernel(const FwdArgs a) {
     __shared__ float buf[8];
@@ -871,7 +887,7 @@ Plan plan(int64_t rows, int warps, int threads, int sms, int shared, int row, in
     while (groups > 0 && shared + groups * few * row > kSmemBytes) --groups;
     if (groups == 0) return p;
     p.groups = groups;
-    p.stages = shared + groups * stages * row > kSmemBytes ? few : stages;
+    p.stages = shared + groups * stages * row > kManyBytes ? few : stages;
     const int64_t need = (rows + groups - 1) / groups;
     p.grid = (int)(need < sms ? need : sms);
     p.threads = 32 * warps * groups;
@@ -942,12 +958,15 @@ bool run_bwd(const BwdArgs& a, int64_t wc, int sms, float* part, cudaStream_t s,
 template <typename T, bool VEC, bool DROP>
 lm_status launch_bwd(const BwdArgs& a, void* dweight, void* dbias, bool accum, float* part,
                      cudaStream_t s) {
-    const int sms = sm_count();
+    int sms = sm_count();
     if (sms <= 0 && a.rows > 0) return LM_ERR_CUDA;
+    if (sms > kMaxParts) sms = kMaxParts;  // a block writes one part
     const bool wgrad = dweight || dbias;
-    // Chunks a thread: two up to 4096 columns (two groups of eight warps a block), four beyond
-    // for bf16 (12288: 178 us with 16384 rows, two chunks and 24 warps 190); one where two
-    // would spill
+    // Chunks a thread: two up to 4096 columns (two or more groups of up to eight warps), four
+    // beyond for bf16 (two groups up to 8192 columns; 16384 x 7168, 113 us, with two chunks
+    // and one group of 14 warps 124; at 12288 two chunks and 24 warps are 190 and four 178).
+    // But two again where they make one group of 15 or 16 warps (8192 x 8192 with
+    // dropout, 108 us, with four chunks and two groups 125).  One where two would spill.
     constexpr bool bf16 = sizeof(typename Elem<T>::raw) == 2;
     constexpr int kTwo = !VEC && DROP && !bf16 ? 1 : 2, kNch = VEC && bf16 ? 4 : kTwo;
     const int64_t wc = (a.cols + kWarpCols - 1) / kWarpCols;
@@ -956,8 +975,9 @@ lm_status launch_bwd(const BwdArgs& a, void* dweight, void* dbias, bool accum, f
         float* const p = wgrad ? part : nullptr;
         timing_mark(s, 'n');
         if (wc == 1    ? run_bwd<T, VEC, 1, DROP>(a, wc, sms, p, s, &parts)
-            : wc <= 16 ? run_bwd<T, VEC, kTwo, DROP>(a, wc, sms, p, s, &parts)
-                       : wc <= 16 * kNch && run_bwd<T, VEC, kNch, DROP>(a, wc, sms, p, s, &parts)) {
+            : wc <= 16 || (wc > 28 && wc <= 32 && kTwo == 2)
+                ? run_bwd<T, VEC, kTwo, DROP>(a, wc, sms, p, s, &parts)
+                : wc <= 16 * kNch && run_bwd<T, VEC, kNch, DROP>(a, wc, sms, p, s, &parts)) {
             if (parts == 0) return LM_ERR_CUDA;
         } else {
             // the weight gradients first: they read dy and s, which dx may overwrite
@@ -995,6 +1015,10 @@ lm_status fwd(FwdArgs a, lm_dtype dtype, bool drop, lm_stream_t stream) {
     bool vec;
     lm_status st = row_access(ts, 6, a.rows, a.cols, dtype, &vec);
     if (st != LM_OK) return st;
+    if (a.rows > 0 && a.s == a.y) return LM_ERR_INVALID_ARG;
+    for (int out = 2; out < 4; ++out)
+        for (int in = 0; in < 2; ++in)
+            if (!in_place_or_apart(ts[out], ts[in], a.rows)) return LM_ERR_INVALID_ARG;
     if (!aligned_to(a.mean, 4) || !aligned_to(a.rstd, 4) || !aligned_to(a.amax, 4))
         return LM_ERR_ALIGNMENT;
     if (a.rows == 0) return LM_OK;
@@ -1026,6 +1050,10 @@ lm_status bwd(BwdArgs a, lm_dtype dtype, bool drop, void* dweight, void* dbias, 
     bool vec;
     lm_status st = row_access(ts, 6, a.rows, a.cols, dtype, &vec);
     if (st != LM_OK) return st;
+    if (a.rows > 0 && a.dx == a.dres) return LM_ERR_INVALID_ARG;
+    for (int out = 3; out < 5; ++out)
+        for (int in = 0; in < 3; ++in)
+            if (!in_place_or_apart(ts[out], ts[in], a.rows)) return LM_ERR_INVALID_ARG;
     const bool accum = flags & LM_NORM_ACCUMULATE_WGRAD;
     const unsigned size = accum || dtype == LM_DTYPE_F32 ? 4 : 2;
     if (!aligned_to(dweight, size) || !aligned_to(dbias, size) || !aligned16(workspace) ||

@@ -47,6 +47,11 @@ inline lm_status row_access(const RowTensor* ts, int n, int64_t rows, int64_t co
     return LM_OK;
 }
 
+// Whether an output may be where an input is: elsewhere, or the same rows.
+inline bool in_place_or_apart(const RowTensor& out, const RowTensor& in, int64_t rows) {
+    return !out.p || out.p != in.p || rows <= 1 || out.ld == in.ld;
+}
+
 // The dropout of probability p: halfwords below round(p 2^16) are dropped.
 inline lm_status dropout_args(double p, const uint64_t* rng, uint64_t offset, Dropout* d) {
     if (!(p >= 0.0 && p <= 1.0) || !rng) return LM_ERR_INVALID_ARG;

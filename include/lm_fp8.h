@@ -219,7 +219,9 @@ typedef enum { LM_DTYPE_BF16 = 0, LM_DTYPE_F32 = 1 } lm_dtype;
  *   m = mean_c X[r][c],  v = mean_c (X[r][c] - m)^2,  rstd = 1 / sqrt(v + eps)
  *   Y[r][c] = (X[r][c] - m) rstd weight[c] + bias[c]
  *
- * Sums in fp32, the variance from the centred values; Y is rounded once.
+ * Sums in fp32, the variance from the centred values; Y is rounded once.  (So the
+ * squares of a row's centred values have to fit fp32, and for the backward
+ * 1 / rstd^2 = v + eps has to be a normal fp32, 1.2e-38 or more.)
  * X, Y: [rows x cols] with row strides ldx, ldy (elements, >= cols); weight,
  * bias: [cols], each may be NULL (1 and 0); mean, rstd: fp32 [rows] for the
  * backward pass, each may be NULL.
@@ -293,7 +295,8 @@ LM_API lm_status lm_dropout_add_bwd(const void* dY, int64_t lddy, int64_t rows, 
  * The end of one branch and the start of the next in one pass:
  *   S = residual + dropout(X)    as lm_dropout_add_fwd
  *   Y = layer norm of S          as lm_layernorm_fwd on the S that is stored
- * S may be X or residual (same pointer and stride).
+ * S may be X or residual, Y may be X or residual where S is not (same pointer and
+ * stride); S and Y are not the same.
  */
 LM_API lm_status lm_dropout_add_layernorm_fwd(const void* X, int64_t ldx, const void* residual,
                                               int64_t ldr, const void* weight, const void* bias,
@@ -349,7 +352,8 @@ typedef struct lm_rope_tensor {
  *   at start + s.
  * rot_dim even, 0 <= rot_dim <= head_dim <= 512; batch x seq < 2^31; heads <=
  *   65536 a tensor; x and y need their element's alignment only.
- *   batch, seq or heads may be 0.  y may be x (same pointer and strides).
+ *   batch, seq or heads may be 0.  y may be x (same pointer and strides), but neither
+ *   the other tensor's x nor its y.
  */
 LM_API lm_status lm_rope(const lm_rope_tensor* tensors, int count, int64_t batch, int64_t seq,
                          int64_t head_dim, int64_t rot_dim, lm_dtype dtype,

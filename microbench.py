@@ -31,6 +31,11 @@ iterations).  Also the small, self-contained command to run under ncu.
         (one optimizer step of gradient accumulation: the weights are cast by the
         first micro-batch's forward and reused by the others; every backward adds
         its weight gradients into fp32 accumulators)
+    python microbench.py rows --rows 16384 --cols 4096 [--dtype f32] [--p 0.1]
+        (the row operators between the GEMMs, forward and backward: layer norm, dropout
+        into the residual stream, and the two in one pass)
+    python microbench.py rope --batch 8 --seq 2048 --heads 24 --kv-heads 8 --head-dim 128
+        (rotary positions of Q and K, and the inverse)
 """
 import argparse
 import json
@@ -164,11 +169,62 @@ def linears(a, gen, flush):
     return res
 
 
+def rows(a, gen, flush):
+    """Layer norm, dropout and the two in one pass, through api: us and GB/s each."""
+    from fp8_gemms_b200 import api
+    dt = torch.float32 if a.dtype == "f32" else torch.bfloat16
+    draw = lambda *s: torch.randn(*s, device="cuda", generator=gen).to(dt)
+    x, r, dy, ds = (draw(a.rows, a.cols) for _ in range(4))
+    w, b, rng = draw(a.cols), draw(a.cols), api.dropout_rng(1)
+    _, mean, rstd = api.layernorm(x, w, b)
+    calls = [("layernorm", 2, lambda: api.layernorm(x, w, b)),
+             ("layernorm_backward", 3, lambda: api.layernorm_backward(dy, x, w, mean, rstd)),
+             ("dropout_add", 3, lambda: api.dropout_add(x, a.p, rng, residual=r)),
+             ("dropout_add_backward", 2, lambda: api.dropout_add_backward(dy, a.p, rng)),
+             ("dropout_add_layernorm", 4,
+              lambda: api.dropout_add_layernorm(x, r, w, b, a.p, rng)),
+             ("dropout_add_layernorm_backward", 5,
+              lambda: api.dropout_add_layernorm_backward(dy, ds, x, w, mean, rstd, a.p, rng))]
+    out = dict(op="rows", rows=a.rows, cols=a.cols, dtype=a.dtype, p=a.p)
+    for name, passes, fn in calls:
+        ms = sorted(time_it(fn, a.iters, a.warmup, flush))[a.iters // 2]
+        out[name] = dict(us=round(ms * 1e3, 2),
+                         gbs=round(passes * x.numel() * x.element_size() / ms / 1e6, 1))
+    return out
+
+
+def rope(a, gen, flush):
+    from fp8_gemms_b200 import api
+    dt = torch.float32 if a.dtype == "f32" else torch.bfloat16
+    q, k = (torch.randn(a.batch, a.seq, h, a.head_dim, device="cuda", generator=gen).to(dt)
+            for h in (a.heads, a.kv_heads))
+    freq, mag = api.rope_frequencies(a.rot_dim or a.head_dim)
+    pos = torch.arange(a.seq, device="cuda").repeat(a.batch, 1)
+    out = dict(op="rope", batch=a.batch, seq=a.seq, heads=a.heads, kv_heads=a.kv_heads,
+               head_dim=a.head_dim, rot_dim=2 * freq.shape[0], interleaved=a.interleaved,
+               dtype=a.dtype)
+    for name, fn in (("rope", api.rope), ("rope_backward", api.rope_backward)):
+        call = lambda: fn([q, k], freq, positions=pos, interleaved=a.interleaved, magnitude=mag)
+        ms = sorted(time_it(call, a.iters, a.warmup, flush))[a.iters // 2]
+        byts = 2 * (q.numel() + k.numel()) * q.element_size()
+        out[name] = dict(us=round(ms * 1e3, 2), gbs=round(byts / ms / 1e6, 1))
+    return out
+
+
 def main():
     p = argparse.ArgumentParser()
     p.add_argument("op", choices=["gemm", "cast", "mlp-accum", "mlp-fwd", "rmsnorm-cast",
                                   "mlp-compare", "lmhead-ce", "scaled-mm", "torch-composition",
-                                  "linears"])
+                                  "linears", "rows", "rope"])
+    p.add_argument("--dtype", default="bf16", choices=["bf16", "f32"])
+    p.add_argument("--p", type=float, default=0.1, help="rows: the dropout probability")
+    p.add_argument("--batch", type=int, default=8)
+    p.add_argument("--seq", type=int, default=2048)
+    p.add_argument("--heads", type=int, default=24)
+    p.add_argument("--kv-heads", type=int, default=8)
+    p.add_argument("--head-dim", type=int, default=128)
+    p.add_argument("--rot-dim", type=int, default=0, help="rope: 0 turns whole heads")
+    p.add_argument("--interleaved", action="store_true")
     p.add_argument("--workload", default="attn-head", choices=["attn-head", "stack"])
     p.add_argument("--layers", type=int, default=28)
     p.add_argument("--V", type=int, default=50304)
@@ -213,6 +269,8 @@ def main():
                    tflops=round(2 * 2 * M * d * f / avg / 1e9, 1))
     elif a.op == "linears":
         out = linears(a, gen, flush)
+    elif a.op in ("rows", "rope"):
+        out = {"rows": rows, "rope": rope}[a.op](a, gen, flush)
     elif a.op == "scaled-mm":
         # (name, M, N, K, A format, B format, operand storage in the step)
         shapes = [("up", 16384, 12288, 3072, E4M3, E4M3, 0),

@@ -89,7 +89,8 @@ def test_layernorm_fwd_refusals(L):
     assert call(rows=0) == 0 and call(rows=0, x=None, y=None) == 0
     assert call(dt=7) == 4
     for bad in [dict(x=None), dict(y=None), dict(rows=-1), dict(cols=0), dict(cols=-8),
-                dict(eps=-1.0), dict(eps=float("nan")), dict(ldx=63), dict(ldy=0), dict(ldy=-64)]:
+                dict(eps=-1.0), dict(eps=float("nan")), dict(ldx=63), dict(ldy=0), dict(ldy=-64),
+                dict(ldy=72)]:   # y over x with another stride
         assert call(**bad) == 1, bad
     for bad in [dict(x=FAKE + 1), dict(y=FAKE + 1), dict(w=FAKE + 1), dict(mean=FAKE + 2),
                 dict(rstd=FAKE + 1), dict(amax=FAKE + 2), dict(x=FAKE + 2, dt=F32)]:
@@ -131,7 +132,7 @@ def test_dropout_refusals(L):
     assert call(rows=0) == 0
     assert call(dt=2) == 4
     for bad in [dict(p=-0.1), dict(p=1.1), dict(p=float("nan")), dict(rng=None), dict(x=None),
-                dict(y=None), dict(rows=-1), dict(cols=0), dict(ldr=0), dict(ldx=1)]:
+                dict(y=None), dict(rows=-1), dict(cols=0), dict(ldr=0), dict(ldx=1), dict(ldy=80)]:
         assert call(**bad) == 1, bad
     for bad in [dict(rng=FAKE + 4), dict(x=FAKE + 1), dict(r=FAKE + 1), dict(y=FAKE + 2, dt=F32)]:
         assert call(**bad) == 2, bad
@@ -142,7 +143,7 @@ def test_dropout_refusals(L):
 
 
 def test_dropout_layernorm_refusals(L):
-    def fwd(x=FAKE, r=FAKE, s=FAKE, y=FAKE, p=0.1, rng=FAKE, lds=64, rows=4):
+    def fwd(x=FAKE, r=FAKE, s=FAKE, y=FAKE + 0x10000, p=0.1, rng=FAKE, lds=64, rows=4):
         return L.lib.lm_dropout_add_layernorm_fwd(x, 64, r, 64, FAKE, FAKE, rows, 64, 1e-5, BF16, p,
                                                   rng, 0, s, lds, y, 64, FAKE, FAKE, None, None)
     assert fwd(rows=0) == 0
@@ -150,14 +151,15 @@ def test_dropout_layernorm_refusals(L):
                 dict(lds=8)]:
         assert fwd(**bad) == 1, bad
     assert fwd(s=FAKE + 1) == 2
+    assert fwd(y=FAKE) == 1                       # y where s is
     n = L.lm_layernorm_workspace_size(4, 64)
 
-    def bwd(dy=FAKE, ds=FAKE, s=FAKE, dx=FAKE, dr=FAKE, p=0.1, rng=FAKE, ws=FAKE, nb=n):
+    def bwd(dy=FAKE, ds=FAKE, s=FAKE, dx=FAKE, dr=FAKE + 0x10000, p=0.1, rng=FAKE, ws=FAKE, nb=n):
         return L.lib.lm_dropout_add_layernorm_bwd(dy, 64, ds, 64, s, 64, FAKE, FAKE, FAKE, 4, 64,
                                                   BF16, p, rng, 0, dx, 64, dr, 64, FAKE, FAKE, ws,
                                                   nb, 0, None)
     for bad in [dict(dy=None), dict(s=None), dict(dx=None), dict(dr=None), dict(p=-1.0),
-                dict(rng=None), dict(ws=None), dict(nb=n - 1)]:
+                dict(rng=None), dict(ws=None), dict(nb=n - 1), dict(dr=FAKE)]:
         assert bwd(**bad) == 1, bad
     assert bwd(ds=FAKE + 1) == 2 and bwd(rng=FAKE + 4) == 2
 
@@ -182,6 +184,11 @@ def test_rope_refusals(L):
                 # outputs that overlap: heads 32 apart, one row for all tokens, batches folded
                 dict(ts=[tensor(ys=(2048, 256, 32))]), dict(ts=[tensor(ys=(2048, 0, 64))]),
                 dict(ts=[tensor(ys=(1024, 256, 64))]), dict(ts=[tensor(ys=(2048, 256, -64))]),
+                # one output for both, an output over the other's input
+                dict(ts=[tensor(), tensor(x=FAKE + 0x300000)]),
+                dict(ts=[tensor(), tensor(x=FAKE + 0x300000, y=FAKE)]),
+                dict(ts=[tensor(), tensor(x=FAKE + 0x100000, y=FAKE + 0x300000)]),
+                dict(start=(1 << 63) - 5),
                 # in place with other strides
                 dict(ts=[tensor(y=FAKE, xs=(2048, 64, 512))])]:
         assert call(**bad) == 1, bad
