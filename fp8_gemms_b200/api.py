@@ -16,16 +16,18 @@ libfp8lm.so does every step of the computation.
     inv_freq, magnitude = api.rope_frequencies(head_dim)
     q, k = api.rope([q, k], inv_freq, magnitude=magnitude)
 """
-import functools
-
 import torch
 
 from . import _lib
 from ._lib import (E4M3, E5M2, EPI_ACCUM_F32, EPI_NONE, EPI_RELU2_BWD,  # noqa: F401
                    EPI_RELU2_FWD, GEMM_A_MN_MAJOR, GEMM_B_MN_MAJOR, LINEAR_ACCUMULATE_WGRAD,
                    LINEAR_REUSE_WEIGHT_CAST, MLP_ACCUMULATE_WGRAD, MLP_REUSE_WEIGHT_CASTS,
-                   NORM_ACCUMULATE_WGRAD, ROPE_BY_PARTS, ROPE_INTERLEAVED, ROPE_INVERSE,
-                   ROPE_LINEAR, ROPE_NTK, ROPE_UNSCALED, LmError)
+                   ROPE_BY_PARTS, ROPE_LINEAR, ROPE_NTK, ROPE_UNSCALED, LmError)
+
+try:
+    from . import _native
+except ImportError as e:
+    raise ImportError(f"_native.so ({e}); run `python -m fp8_gemms_b200.build`") from e
 
 
 def _dev(t):
@@ -359,64 +361,35 @@ def linear_fwd_bwd(X, W, dY, stream=None):
 
 
 # ------------------------------------------------- operators between the GEMMs
-def _placed(fn):
-    """Runs fn on its first tensor's device and on `stream` (a torch.cuda.Stream;
-    None: that device's current one), where the outputs and workspaces are
-    allocated too."""
-    @functools.wraps(fn)
-    def placed(x, *args, stream=None, **kw):
-        t = x[0] if isinstance(x, (list, tuple)) else x
-        if not t.is_cuda or (stream is None and t.get_device() == torch._C._cuda_getDevice()):
-            return fn(x, *args, **kw)  # a host tensor is refused by the call itself
-        device = t.device
-        with torch.cuda.device(device):
-            with torch.cuda.stream(stream or torch.cuda.current_stream(device)):
-                return fn(x, *args, **kw)
-    return placed
+# _native (csrc/binding.cpp) checks the arguments, allocates what is not given and makes
+# the C call on the current stream of the tensors' device.  stream: a torch.cuda.Stream
+# to run on instead, where the outputs and workspaces are allocated too.
+_native.use_error(LmError)
 
 
-def _stats(x):
-    if x.dim() != 2:
-        _lib._refuse("the rows' statistics", "a 2-D CUDA tensor is wanted")
-    mean = x.new_empty(x.shape[0], dtype=torch.float32)
-    return mean, torch.empty_like(mean)
+def _call(fn, stream, *args):
+    if stream is None:
+        return fn(*args)
+    first = args[0] if isinstance(args[0], torch.Tensor) else args[0][0]
+    if stream.device != first.device:
+        raise LmError(1, f"{fn.__name__}: the stream is of another device")
+    with torch.cuda.stream(stream):
+        return fn(*args)
 
 
-def _wgrads(x, dweight, dbias, accumulate):
-    """dweight, dbias and the workspace of a norm's backward."""
-    if x.dim() != 2:
-        _lib._refuse("the weight gradients", "a 2-D CUDA tensor is wanted")
-    rows, cols = x.shape
-    if not accumulate:
-        if dweight is None:
-            dweight = x.new_empty(cols)
-        if dbias is None:
-            dbias = torch.empty_like(dweight)
-    ws = x.new_empty(_lib.lib.lm_layernorm_workspace_size(rows, cols), dtype=torch.uint8)
-    return dweight, dbias, ws
-
-
-@_placed
-def layernorm(x, weight=None, bias=None, eps=1e-5, out=None, amax_out=None):
+def layernorm(x, weight=None, bias=None, eps=1e-5, out=None, amax_out=None, stream=None):
     """Layer norm of [rows x cols] bf16 or fp32.  Returns (y, mean, rstd), the
     statistics fp32 [rows] for layernorm_backward.  amax_out: a zeroed fp32
     that receives max |y|, the amax_in of a following cast()."""
-    y = torch.empty_like(x) if out is None else out
-    mean, rstd = _stats(x)
-    _lib.lm_layernorm_fwd(x, weight, bias, y, mean, rstd, eps, amax_out)
-    return y, mean, rstd
+    return _call(_native.layernorm, stream, x, weight, bias, eps, out, amax_out)
 
 
-@_placed
 def layernorm_backward(dy, x, weight, mean, rstd, out=None, dweight=None, dbias=None,
-                       accumulate=False):
+                       accumulate=False, stream=None):
     """Returns (dx, dweight, dbias), the latter two of x's type.  With accumulate,
     dweight and dbias are given fp32 accumulators (or None) that are added to."""
-    dx = torch.empty_like(x) if out is None else out
-    dweight, dbias, ws = _wgrads(x, dweight, dbias, accumulate)
-    _lib.lm_layernorm_bwd(dy, x, weight, mean, rstd, dx, dweight, dbias, ws,
-                          NORM_ACCUMULATE_WGRAD if accumulate else 0)
-    return dx, dweight, dbias
+    return _call(_native.layernorm_backward, stream, dy, x, weight, mean, rstd, out, dweight,
+                 dbias, accumulate)
 
 
 def dropout_rng(seed, offset=0, device="cuda"):
@@ -427,44 +400,30 @@ def dropout_rng(seed, offset=0, device="cuda"):
     return torch.tensor(signed, dtype=torch.int64, device=device)
 
 
-@_placed
-def dropout_add(x, p, rng, offset=0, residual=None, out=None):
+def dropout_add(x, p, rng, offset=0, residual=None, out=None, stream=None):
     """residual + dropout(x) (plain dropout without a residual)."""
-    y = torch.empty_like(x) if out is None else out
-    _lib.lm_dropout_add_fwd(x, residual, y, p, rng, offset)
-    return y
+    return _call(_native.dropout_add, stream, x, p, rng, offset, residual, out)
 
 
-@_placed
-def dropout_add_backward(dy, p, rng, offset=0, out=None):
+def dropout_add_backward(dy, p, rng, offset=0, out=None, stream=None):
     """dx of dropout_add (the residual's gradient is dy itself)."""
-    dx = torch.empty_like(dy) if out is None else out
-    _lib.lm_dropout_add_bwd(dy, dx, p, rng, offset)
-    return dx
+    return _call(_native.dropout_add_backward, stream, dy, p, rng, offset, out)
 
 
-@_placed
-def dropout_add_layernorm(x, residual, weight, bias, p, rng, offset=0, eps=1e-5, amax_out=None):
+def dropout_add_layernorm(x, residual, weight, bias, p, rng, offset=0, eps=1e-5, amax_out=None,
+                          stream=None):
     """s = residual + dropout(x) and its layer norm y in one pass.  Returns
     (s, y, mean, rstd)."""
-    s, y = torch.empty_like(x), torch.empty_like(x)
-    mean, rstd = _stats(x)
-    _lib.lm_dropout_add_layernorm_fwd(x, residual, weight, bias, s, y, p, rng, offset, mean, rstd,
-                                      eps, amax_out)
-    return s, y, mean, rstd
+    return _call(_native.dropout_add_layernorm, stream, x, residual, weight, bias, p, rng, offset,
+                 eps, amax_out)
 
 
-@_placed
 def dropout_add_layernorm_backward(dy, ds, s, weight, mean, rstd, p, rng, offset=0, dweight=None,
-                                   dbias=None, accumulate=False):
+                                   dbias=None, accumulate=False, stream=None):
     """From dy and ds (the gradient of s from the stream after it, or None):
     (dx, dresidual, dweight, dbias)."""
-    dx, dr = torch.empty_like(s), torch.empty_like(s)
-    dweight, dbias, ws = _wgrads(s, dweight, dbias, accumulate)
-    _lib.lm_dropout_add_layernorm_bwd(dy, ds, s, weight, mean, rstd, p, rng, dx, dr, dweight,
-                                      dbias, ws, offset,
-                                      NORM_ACCUMULATE_WGRAD if accumulate else 0)
-    return dx, dr, dweight, dbias
+    return _call(_native.dropout_add_layernorm_backward, stream, dy, ds, s, weight, mean, rstd, p,
+                 rng, offset, dweight, dbias, accumulate)
 
 
 def rope_frequencies(rot_dim, theta=10000.0, scaling=ROPE_UNSCALED, factor=1.0, context=0.0,
@@ -475,24 +434,18 @@ def rope_frequencies(rot_dim, theta=10000.0, scaling=ROPE_UNSCALED, factor=1.0, 
     return torch.tensor(freqs, dtype=torch.float64, device=device), magnitude
 
 
-def _rope(xs, inv_freq, positions, start, interleaved, magnitude, out, flags):
-    ys = [torch.empty_like(x) for x in xs] if out is None else out
-    _lib.lm_rope(xs, ys, inv_freq, positions, start, magnitude,
-                 flags | (ROPE_INTERLEAVED if interleaved else 0))
-    return ys
-
-
-@_placed
-def rope(xs, inv_freq, positions=None, start=0, interleaved=False, magnitude=1.0, out=None):
+def rope(xs, inv_freq, positions=None, start=0, interleaved=False, magnitude=1.0, out=None,
+         stream=None):
     """Rotary positions of one or two [batch, seq, heads, head_dim] tensors (Q and
     K), any strides but adjacent elements; the first 2 len(inv_freq) elements of
     each head turn.  positions: int64 [batch, seq], or None for start + s.
     Returns the list of outputs (`out` may be `xs`: in place)."""
-    return _rope(xs, inv_freq, positions, start, interleaved, magnitude, out, 0)
+    return _call(_native.rope, stream, xs, inv_freq, positions, start, interleaved, magnitude, out,
+                 False)
 
 
-@_placed
 def rope_backward(dys, inv_freq, positions=None, start=0, interleaved=False, magnitude=1.0,
-                  out=None):
+                  out=None, stream=None):
     """The gradients of rope()'s inputs from those of its outputs."""
-    return _rope(dys, inv_freq, positions, start, interleaved, magnitude, out, ROPE_INVERSE)
+    return _call(_native.rope, stream, dys, inv_freq, positions, start, interleaved, magnitude, out,
+                 True)

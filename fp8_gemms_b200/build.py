@@ -1,4 +1,5 @@
-"""Build libfp8lm.so (the C-ABI library) in-tree with nvcc for sm_100a.
+"""Build libfp8lm.so (the C-ABI library) in-tree with nvcc for sm_100a, and
+_native.so (csrc/binding.cpp, the Python calls of the operators between the GEMMs) with g++.
 
     python -m fp8_gemms_b200.build [--force] [--verbose]
 
@@ -9,12 +10,15 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfp8lm.so")
+BINDING = os.path.join(CSRC, "binding.cpp")
+NATIVE = os.path.join(PKG, "_native.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -37,7 +41,36 @@ def _stale():
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def build_native(force: bool = False) -> str:
+    """The Python module beside the library; built for the torch that is installed."""
+    deps = [BINDING, os.path.join(INCLUDE, "lm_fp8.h")]
+    if (not force and os.path.exists(NATIVE)
+            and all(os.path.getmtime(p) <= os.path.getmtime(NATIVE) for p in deps)):
+        return NATIVE
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api",
+                                                       "include"),
+           os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include"),
+           sysconfig.get_paths()["include"], INCLUDE]
+    tmp = NATIVE + ".tmp"
+    subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+                    "-fvisibility=hidden", "-Wno-deprecated-declarations",
+                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                    *[f"-I{p}" for p in inc], BINDING, "-o", tmp, f"-L{PKG}", "-lfp8lm",
+                    "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+                    "-lc10_cuda", "-Wl,-rpath,$ORIGIN"], check=True)
+    os.replace(tmp, NATIVE)
+    return NATIVE
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_library(force, verbose)
+    build_native(force)
+    return LIB
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")

@@ -910,7 +910,8 @@ bool allow_smem(K kernel, bool (&done)[64]) {
 // wc: chunks of 256 columns.  A warp takes four, which leaves the least to add up between
 // warps; up to 1024 columns that is the whole row.  Without VEC it takes two (a
 // chunk's eight scalar accesses need the registers).  Few rows go one chunk a warp, for
-// the shortest path: 16 x 1024 in 2.3 us instead of 2.9.
+// the shortest path: bf16 16 x 1024 in 2.0 us instead of 2.7, 148 x 4096 in 2.5 instead of
+// 3.0; fused, 128 x 768 in 2.2 instead of 3.3.
 template <typename T, bool VEC, bool DROP>
 lm_status launch_fwd(const FwdArgs& a, cudaStream_t s) {
     const int sms = sm_count();

@@ -249,3 +249,27 @@ def test_gradient_formulas_against_differences():
     for il in (False, True):
         a = (ref.rope(x, f, pos, il, 1.2) * dy).sum()
         assert math.isclose(a, (x * ref.rope(dy, f, pos, il, 1.2, inverse=True)).sum(), rel_tol=1e-12)
+
+
+def test_a_stream_of_another_device_is_refused():
+    from types import SimpleNamespace
+    from fp8_gemms_b200 import api
+    stream = SimpleNamespace(device=torch.device("cuda", 1))
+    q = torch.zeros(1, 2, 1, 8)
+    for call in (lambda: api.layernorm(q[0, :, 0], stream=stream),
+                 lambda: api.rope([q], torch.ones(4, dtype=torch.float64), stream=stream)):
+        with pytest.raises(api.LmError) as e:
+            call()
+        assert e.value.status == 1
+
+
+def test_arguments_that_are_no_tensors_are_refused():
+    from fp8_gemms_b200 import api
+    for call in (lambda: api.layernorm([1.0]), lambda: api.dropout_add(None, 0.1, None),
+                 lambda: api.rope([], None), lambda: api.rope([None], None),
+                 lambda: api.rope([torch.zeros(1, 1, 1, 2)] * 3, None)):
+        with pytest.raises(api.LmError) as e:
+            call()
+        assert e.value.status == 1
+    with pytest.raises(TypeError):
+        api.rope(3, None)
