@@ -7,8 +7,9 @@
 // residual; without one the generator and the selections come close (the ALU pipe 65%
 // busy, 28.6 M warp instructions for 16384 x 4096 against 43 M before the whole-tile kernel).
 // One B200, back to back for some ms, of a copy's 6.46 TB/s: 16384 x 12288 bf16 125 us (100%),
-// with a residual 171 us (110%); 8192 x 8192 fp32 78 us (107%).  A width of 1001 (bf16,
-// 2-byte accesses, each row at another alignment) reaches a third of that.
+// with a residual 171 us (110%); 8192 x 8192 fp32 78 us (107%).  Odd bf16
+// widths, each row at another alignment: 16384 x 4095 69 us (61%; the generator and the bits'
+// way to their elements), with a residual 83 us (75%), by 2-byte accesses 119 and 148.
 #include "lm_chunk.cuh"
 #include "lm_internal.h"
 #include "lm_philox.cuh"
@@ -135,6 +136,102 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropArgs a, int acro
     }
 }
 
+// The elements of a lane's aligned eight that lie in a row of `cols` columns: one access where
+// all do, else one each.  The first is column `col`, which may be before the row.
+template <typename T>
+__device__ __forceinline__ void load_within(Chunk<T>& c, const void* row, int col, int cols) {
+    const typename Elem<T>::raw* p = static_cast<const typename Elem<T>::raw*>(row) + col;
+    if (col >= 0 && col + kChunk <= cols) {
+        ld_vec(c, p);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < Elem<T>::kWords; ++i) c.w[i] = 0u;
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) {
+        const uint32_t v = col + j >= 0 && col + j < cols ? (uint32_t)p[j] : 0u;
+        if constexpr (sizeof(*p) == 4)
+            c.w[j] = v;
+        else
+            c.w[j >> 1] |= v << (16 * (j & 1));
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store_within(void* row, int col, int cols, const Chunk<T>& c) {
+    typename Elem<T>::raw* p = static_cast<typename Elem<T>::raw*>(row) + col;
+    if (col >= 0 && col + kChunk <= cols) {
+        st_vec(p, c);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j)
+        if (col + j >= 0 && col + j < cols) {
+            if constexpr (sizeof(*p) == 4)
+                p[j] = c.w[j];
+            else
+                p[j] = (uint16_t)(c.w[j >> 1] >> (16 * (j & 1)));
+        }
+}
+
+// Rows of any width whose tensors lie alike: row r starts `shift` elements (0..7) past a
+// boundary of eight in each of them, as whole tensors of an odd width do.  Aligned
+// eight q of a row is its columns 8 q - shift .. + 7; their bits are those of
+// column groups q - 1 and q, of which a lane makes q and the lane before it q - 1.  A warp takes
+// kTiles x 32 - 1 eights of a row; its first lane starts with a group for the next lane only.
+// (The ends of the rows an element a lane, gathered by shuffles, took 80 registers instead of 44
+// and 76 us at 16384 x 4095 instead of 69.)
+template <typename T, bool ADD>
+__global__ void __launch_bounds__(256) dropout_shifted_kernel(const DropArgs a, uint32_t across,
+                                                              uint32_t shift0) {
+    constexpr int kTiles = tiles_of_warp<T>();
+    const int lane = threadIdx.x & 31, cols = (int)a.cols;
+    const int64_t task = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int64_t row = task >> 32 == 0 ? (uint32_t)task / across : task / across;
+    if (row >= a.rows) return;
+    const int q0 = (int)(task - row * across) * (32 * kTiles - 1) - 1;
+    const uint32_t shift = (shift0 + (uint32_t)row * (uint32_t)a.ldx) & 7;
+    const int first = kChunk * (q0 + lane) - (int)shift;  // this lane's first column
+    const void* const x = row_at<T>(a.x, row, a.ldx);
+    const void* const res = ADD ? row_at<T>(a.residual, row, a.ldr) : nullptr;
+    Chunk<T> c[kTiles], r[kTiles];
+#pragma unroll
+    for (int k = 0; k < kTiles; ++k) {
+        const int col = first + k * kWarpCols;
+        if (col < cols && (k > 0 || lane > 0)) {
+            load_within(c[k], x, col, cols);
+            if (ADD) load_within(r[k], res, col, cols);
+        }
+    }
+    const PhiloxKey key = philox_key(a.drop);
+    void* const y = row_at<T>(a.y, row, a.ldy);
+    uint32_t last = 0;
+#pragma unroll
+    for (int k = 0; k < kTiles; ++k) {
+        if (kChunk * (q0 + 32 * k) - (int)shift >= cols) break;  // the same for the warp
+        const uint32_t m = group_bits(key, a.drop, (uint32_t)row, (uint32_t)(q0 + 32 * k + lane));
+        const uint32_t before = __shfl_sync(0xFFFFFFFFu, lane == 31 ? last : m, (lane + 31) & 31);
+        last = m;
+        const Keep<false> keep = {((m << 8) | before) >> (8 - shift)};
+        const int col = first + k * kWarpCols;
+        if (col < cols && (k > 0 || lane > 0)) {
+            drop_chunk<ADD>(c[k], r[k], keep, a.drop);
+            store_within(y, col, cols, c[k]);
+        }
+    }
+}
+
+// Elements past a boundary of eight, of a tensor's first row.
+template <typename T>
+uint32_t past_eight(const void* p) {
+    return (uint32_t)((uintptr_t)p / sizeof(typename Elem<T>::raw)) & 7;
+}
+template <typename T>
+bool lie_alike(const DropArgs& a) {
+    const uint32_t shift = past_eight<T>(a.x);
+    return past_eight<T>(a.y) == shift && ((a.ldy - a.ldx) & 7) == 0 &&
+           (!a.residual || (past_eight<T>(a.residual) == shift && ((a.ldr - a.ldx) & 7) == 0));
+}
+
 template <typename T, bool ADD>
 lm_status launch(const DropArgs& a, bool vec, cudaStream_t s) {
     constexpr int kTiles = tiles_of_warp<T>();
@@ -144,6 +241,22 @@ lm_status launch(const DropArgs& a, bool vec, cudaStream_t s) {
         timing_mark(s, 'd');
         dropout_full_kernel<T, ADD><<<(unsigned)blocks, 256, 0, s>>>(a, (uint32_t)across);
         return launch_status();
+    }
+    // Up to 256 columns the row's two ends cost more than the wide accesses save (65536 x 250
+    // bf16 45 us instead of 34, x 300 42 instead of 52); fp32 beside a residual is at the copy's rate
+    // with scalar accesses, and below it here up to a thousand columns.
+    if constexpr (sizeof(typename Elem<T>::raw) == 2 || !ADD) {
+        if (!vec && a.cols > kWarpCols && lie_alike<T>(a)) {
+            // a row's eights where it starts 7 past a boundary
+            const int64_t eights = (a.cols + 14) / 8;
+            const int64_t across = (eights + 32 * kTiles - 2) / (32 * kTiles - 1);
+            const int64_t blocks = (a.rows * across + 7) / 8;
+            if (blocks >= (int64_t(1) << 31)) return LM_ERR_UNSUPPORTED_SHAPE;
+            timing_mark(s, 'd');
+            dropout_shifted_kernel<T, ADD>
+                <<<(unsigned)blocks, 256, 0, s>>>(a, (uint32_t)across, past_eight<T>(a.x));
+            return launch_status();
+        }
     }
     const int across = (int)((a.cols + kWarpCols - 1) / kWarpCols);
     const int rows_in = vec && a.cols <= 128 ? (int)(256 / a.cols) : 1;

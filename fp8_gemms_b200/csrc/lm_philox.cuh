@@ -105,26 +105,32 @@ struct Keep<false> {
     uint32_t bits;
 };
 
+// The eight elements of column group `group`: bit j for its column j.
+template <typename Key>
+__device__ __forceinline__ uint32_t group_bits(const Key& key, const Dropout& d, uint32_t row,
+                                               uint32_t group) {
+    uint32_t w[4], m = 0;
+    philox(key, group, row, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        // the upper half as it is (what is below does not change the comparison), the
+        // lower half moved up
+        const uint32_t h = (j & 1) ? w[j >> 1] : w[j >> 1] << 16;
+        m |= (h >= d.least && d.live ? 1u : 0u) << j;
+    }
+    return m;
+}
+
 // group: the row's eighth column group that this lane makes the words of, base / 8 + lane
 // for the warp's 256 columns at `base`.  Every lane calls it.
 template <bool VEC, typename Key>
 __device__ __forceinline__ Keep<VEC> keep_at(const Key& key, const Dropout& d, uint32_t row,
                                              uint32_t group, int lane) {
-    uint32_t w[4];
-    philox(key, group, row, w);
     Keep<VEC> k;
     if constexpr (VEC) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) k.w[i] = w[i];
+        philox(key, group, row, k.w);
     } else {
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            // the upper half as it is (what is below does not change the comparison), the
-            // lower half moved up
-            const uint32_t h = (j & 1) ? w[j >> 1] : w[j >> 1] << 16;
-            m |= (h >= d.least && d.live ? 1u : 0u) << j;
-        }
+        const uint32_t m = group_bits(key, d, row, group);
         k.bits = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {

@@ -53,6 +53,34 @@ def test_bit_for_bit(rows, cols, dtype, pad, shift, p):
         assert not api.dropout_add(x, p, rng()).any()
 
 
+# widths about a warp's 127 (bf16) and 63 (fp32) aligned eights of a row, and about one eight
+@pytest.mark.parametrize("cols", [1, 2, 7, 8, 9, 15, 17, 248, 257, 497, 504, 505, 512, 1001, 1009, 1010,
+                                  1016, 1017, 1024, 2033, 5001])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_that_start_alike_between_the_eights(dtype, cols):
+    """x, residual and output at one distance past an aligned eight, row by row: each first
+    row's distance, with row strides that move it on (odd) and that keep it (a multiple of
+    8); then one of the three lies elsewhere.  Bit for bit; what is between the rows stays."""
+    from fp8_gemms_b200 import api
+    rows = 11
+    for shift in range(8):
+        for pad in (1 + cols % 2, -cols % 8 + 8):
+            x, r = draw((rows, cols), dtype, 1, pad=pad, shift=shift), draw((rows, cols), dtype, 2, 2.0,
+                                                                            pad=pad, shift=shift)
+            want = expected(x, 0.4, 7, r)[0]
+            for other in (0, 3):
+                ld = cols + pad
+                buf = torch.full((shift + other + rows * ld + 64,), float("nan"), dtype=dtype,
+                                 device="cuda")
+                out = buf[shift + other:shift + other + rows * ld].view(rows, ld)[:, :cols]
+                api.dropout_add(x, 0.4, rng(), 7, residual=r, out=out)
+                assert torch.equal(out, want), (shift, pad, other)
+                api.dropout_add_backward(x, 0.4, rng(), 7, out=out)
+                assert torch.equal(out, expected(x, 0.4, 7)[0]), (shift, pad, other)
+                out.fill_(float("nan"))
+                assert torch.isnan(buf).all(), (shift, pad, other)
+
+
 @pytest.mark.parametrize("p,drop", [(2.0 ** -18, 0), (2.0 ** -16, 1), (1.5 * 2.0 ** -16, 2),
                                     (1 - 2.0 ** -16, 65535), (1 - 2.0 ** -18, 65536)])
 def test_probabilities_at_the_ends(p, drop):
