@@ -19,6 +19,10 @@ SHAPES = [(1, 1, 1, 1, 2, 2, F32, "bshd"), (2, 3, 5, 1, 6, 4, BF, "bshd"),
           (1, 13, 3, 2, 40, 0, BF, "bshd"), (1, 7, 3, 3, 72, 16, BF, "odd"),
           (2, 19, 64, 1, 32, 32, F32, "bshd"), (1, 5, 1, 1, 333, 332, BF, "bshd"),
           (1, 2100, 1, 1, 16, 16, BF, "bshd"), (2, 6, 100, 4, 64, 32, BF, "bhsd")]
+# the copied rest with few tokens and with many, at each width of access
+SHAPES += [(3, 700, 3, 2, 40, 16, BF, "bshd"), (3, 701, 3, 2, 40, 20, BF, "bhsd"), (1, 1301, 2, 1, 23, 6, BF, "odd"),
+           (3, 701, 3, 2, 40, 20, F32, "bshd"), (2, 650, 17, 2, 24, 16, F32, "bhsd"), (1185, 1, 2, 2, 12, 4, BF, "qkv"),
+           (7, 1, 33, 5, 48, 16, BF, "qkv"), (5, 3, 2, 2, 512, 320, BF, "bshd")]
 IDS = ["-".join(str(v).replace("torch.", "") for v in s) for s in SHAPES]
 
 
