@@ -58,7 +58,8 @@ def build_native(force: bool = False) -> str:
                     "-fvisibility=hidden", "-Wno-deprecated-declarations",
                     f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
                     *[f"-I{p}" for p in inc], BINDING, "-o", tmp, f"-L{PKG}", "-lfp8lm",
-                    "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+                    "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu",
+                    "-ltorch_cuda", "-lc10",
                     "-lc10_cuda", "-Wl,-rpath,$ORIGIN"], check=True)
     os.replace(tmp, NATIVE)
     return NATIVE
