@@ -15,8 +15,9 @@
 // sines in registers and takes all heads with them; blocks that shared them through
 // shared memory spent their time at barriers and behind 100 registers a thread (16384 tokens, 24 + 8
 // heads of 128, bf16: 93 us; now 43.5 us, 96% of what a copy reaches).  One token of 64
-// sequences takes 2.7 us: the latency of positions, angles and one access.  Where
-// rot_dim / 2 is odd the accesses are scalar (rot_dim 50 of 128: 113 us).
+// sequences takes 2.5 us: the latency of positions, angles and one access.  Where
+// rot_dim / 2 is odd the accesses are scalar (rot_dim 50 of 128: 113 us), where it is no
+// multiple of 8 two elements wide (100 of 100: 48 us, 34 of them the bytes; fp32 68 of 68).
 #include <type_traits>
 
 #include "lm_chunk.cuh"
@@ -110,10 +111,11 @@ __device__ __forceinline__ void repack(Run<T, V>& r, const float (&v)[V]) {
 // 256 pairs are eight blocks of 32 lanes at most.
 constexpr int64_t kMaxHeadDim = 512, kMaxHeads = 65536;
 constexpr int kWarps = 8;   // of a block
-// Heads whose loads a lane issues together: with V = 8 more would cost blocks of registers.
+// Heads whose loads a lane issues together: with V = 8 more would cost blocks of registers; with V = 2
+// four take 54 us instead of 48 (16384 tokens, 24 + 8 heads of 100, bf16).
 template <int V>
 __host__ __device__ constexpr int at_once() {
-    return V == 8 ? 2 : V == 2 ? 4 : 8;
+    return V == 8 ? 2 : 8;
 }
 
 // How the warps share the work: a warp takes one token, `lanes` items of its heads (V pairs
@@ -166,14 +168,15 @@ __global__ void __launch_bounds__(32 * kWarps) rope_kernel(const RopeArgs a, con
         const int e1 = INTERLEAVED ? 2 * f : f, e2 = INTERLEAVED ? 2 * f + V : f + half;
         Run<T, V> r1[kAtOnce], r2[kAtOnce];
         auto fetch = [&](int h) {
+            if (!works || h >= h1) return;
+            // behind the last head the last one again: a test for each would part the loads
+            // (16384 tokens, 24 + 8 heads of 100, fp32: 131 us instead of 68; 64 tokens lose, bf16 3.5
+            // instead of 2.9, and one test at the fifth head costs 80)
 #pragma unroll
             for (int k = 0; k < kAtOnce; ++k) {
-                const int hk = h + k * p.across;
-                if (works && hk < h1) {
-                    const raw* const x = in_of(hk);
-                    load_run(r1[k], x + e1);
-                    load_run(r2[k], x + e2);
-                }
+                const raw* const x = in_of(min(h + k * p.across, h1 - 1));
+                load_run(r1[k], x + e1);
+                load_run(r2[k], x + e2);
             }
         };
         int h = h0 + sub;
@@ -290,7 +293,7 @@ lm_status launch_rope(const RopeArgs& a, bool interleaved, int copy, cudaStream_
     p.parts = (a.heads + p.each - 1) / p.each;
     // A second warp for the copy is worth it where few tokens leave the warps waiting (64 tokens,
     // 64 of 128, bf16: 2.5 us instead of 3.2; 1024 tokens 4.4 instead of 4.7; 2048 tokens 9.5 instead of
-    // 8.1), and for chunks of fp32 (3999 tokens, 32 of 80: 15.1 instead of 16.2; bf16 8.0 instead of
+    // 8.1), and for chunks of fp32 (3999 tokens, 32 of 80: 14.7 instead of 16.2; bf16 8.0 instead of
     // 7.5).
     p.split = items > 0 && a.rot_dim < a.head_dim &&
               (a.tokens <= (int64_t)sms * 8 || (V == 8 && sizeof(typename Elem<T>::raw) == 4));
