@@ -7,8 +7,9 @@
 //
 // (rotary position embedding: J. Su et al., "RoFormer", 2021); the backward pass
 // is the same with the sine negated.  The angle is taken in turns in fp64,
-// t = position * inv_freq / 2 pi, and only t - rint(t) goes to fp32, so the
-// rotation is right at any position; no table is kept or read.  The other
+// t = position * inv_freq / 2 pi, with the product's rest, and only t - rint(t) goes to fp32:
+// the error does not grow with the position, which is itself held in fp64 (exact to 2^53);
+// no table is kept or read.  The other
 // head_dim - rot_dim elements are copied (not touched in place).
 //
 // Bound by HBM: every element read and written once.  A warp keeps a token's cosines and
@@ -37,13 +38,21 @@ struct RopeArgs {
     float magnitude, sign;
 };
 
+// 1 / 2 pi in two parts.
 constexpr double kInvTwoPi = 0.15915494309189533576888376337251;
+constexpr double kInvTwoPiLow = -9.8393383375912432e-18;
 
-// cos and sin of position * inv_freq, times the magnitude, the sine with `sign`.
+// cos and sin of position * inv_freq, times the magnitude, the sine with `sign`.  One fp64
+// product would be off by 2^-53 of the turns made, 1e-4 of an angle at position 2^40; so
+// inv_freq / 2 pi is held in two parts and what the product's rounding leaves is added to
+// the reduced turn.
 __device__ __forceinline__ float2 cos_sin(double position, double inv_freq, float magnitude,
                                           float sign) {
-    double t = position * (inv_freq * kInvTwoPi);
-    t -= rint(t);
+    const double f = __dmul_rn(inv_freq, kInvTwoPi);
+    const double low = __fma_rn(inv_freq, kInvTwoPiLow, __fma_rn(inv_freq, kInvTwoPi, -f));
+    double t = __dmul_rn(position, f);
+    const double left = __fma_rn(position, low, __fma_rn(position, f, -t));
+    t = (t - rint(t)) + left;
     float c, s;
     sincospif((float)(2.0 * t), &s, &c);
     return make_float2(c * magnitude, s * magnitude * sign);
@@ -195,10 +204,13 @@ __global__ void __launch_bounds__(32 * kWarps) rope_kernel(const RopeArgs a, con
                 turn[2 * i] = make_float2(t.x, t.y);
                 turn[2 * i + 1] = make_float2(t.z, t.w);
             }
-        } else if (works) {
+        } else {
+            // also in lanes without work (the first pairs', unused): with the call in a branch
+            // 16384 tokens of 50 of 128 take 155 us instead of 111
+            const int from = works ? f : 0;
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                turn[i] = cos_sin(pos, a.inv_freq[f + i], a.magnitude, a.sign);
+                turn[i] = cos_sin(pos, a.inv_freq[from + i], a.magnitude, a.sign);
         }
         while (works && h < h1) {
 #pragma unroll

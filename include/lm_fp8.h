@@ -344,8 +344,9 @@ typedef struct lm_rope_tensor {
  *
  *   (x1, x2) -> magnitude (x1 cos a - x2 sin a, x2 cos a + x1 sin a)
  *
- * and the other elements are copied.  The angle is reduced in fp64, the
- * rotation is fp32.  With LM_ROPE_INVERSE x is the gradient of the output and y
+ * and the other elements are copied.  The angle is reduced in fp64, to within
+ * 2^-51 of a turn at any position up to 2^53 (positions are held in fp64; frequencies
+ * of at most 1), the rotation is fp32.  With LM_ROPE_INVERSE x is the gradient of the output and y
  * that of the input.
  * inv_freq: device fp64 [rot_dim / 2], 8-byte aligned (lm_rope_inv_freq).
  * positions: device int64 [batch x seq], or NULL: token s of each sequence is
