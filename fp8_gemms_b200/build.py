@@ -26,6 +26,10 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
     "--expt-relaxed-constexpr",
 ]
+NATIVE_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+                "-Wno-deprecated-declarations"]
+NATIVE_LIBS = ["-lfp8lm", "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda",
+               "-Wl,-rpath,$ORIGIN"]
 
 
 def sources():
@@ -41,27 +45,40 @@ def _stale():
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def _native_key() -> str:
+    """What the module is built for and how, beside its sources: it uses PyTorch's C++ headers and
+    one Python's.  The places of compiler, CUDA and tree are left out: a built tree can be
+    taken to another machine of the same image."""
+    import torch
+    return "\n".join([torch.__version__, str(torch.version.git_version),
+                      str(sysconfig.get_config_var("SOABI")),
+                      str(torch._C._GLIBCXX_USE_CXX11_ABI), *NATIVE_FLAGS, *NATIVE_LIBS])
+
+
 def build_native(force: bool = False) -> str:
-    """The Python module beside the library; built for the torch that is installed."""
+    """The Python module beside the library; built for the torch that is installed, which
+    NATIVE + ".key" records."""
     deps = [BINDING, os.path.join(INCLUDE, "lm_fp8.h")]
-    if (not force and os.path.exists(NATIVE)
-            and all(os.path.getmtime(p) <= os.path.getmtime(NATIVE) for p in deps)):
-        return NATIVE
+    key, key_file = _native_key(), NATIVE + ".key"
+    if not force and os.path.exists(NATIVE) and os.path.exists(key_file):
+        with open(key_file) as f:
+            same = f.read() == key
+        if same and all(os.path.getmtime(p) <= os.path.getmtime(NATIVE) for p in deps):
+            return NATIVE
+    tmp = NATIVE + ".tmp"
     import torch
     root = os.path.dirname(torch.__file__)
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api",
                                                        "include"),
            os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include"),
            sysconfig.get_paths()["include"], INCLUDE]
-    tmp = NATIVE + ".tmp"
-    subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
-                    "-fvisibility=hidden", "-Wno-deprecated-declarations",
+    subprocess.run([os.environ.get("CXX", "g++"), *NATIVE_FLAGS,
                     f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-                    *[f"-I{p}" for p in inc], BINDING, "-o", tmp, f"-L{PKG}", "-lfp8lm",
-                    "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu",
-                    "-ltorch_cuda", "-lc10",
-                    "-lc10_cuda", "-Wl,-rpath,$ORIGIN"], check=True)
+                    *[f"-I{p}" for p in inc], BINDING, "-o", tmp, f"-L{PKG}",
+                    "-L" + os.path.join(root, "lib"), *NATIVE_LIBS], check=True)
     os.replace(tmp, NATIVE)
+    with open(key_file, "w") as f:
+        f.write(key)
     return NATIVE
 
 
