@@ -24,10 +24,23 @@ from ._lib import (E4M3, E5M2, EPI_ACCUM_F32, EPI_NONE, EPI_RELU2_BWD,  # noqa: 
                    LINEAR_REUSE_WEIGHT_CAST, MLP_ACCUMULATE_WGRAD, MLP_REUSE_WEIGHT_CASTS,
                    ROPE_BY_PARTS, ROPE_LINEAR, ROPE_NTK, ROPE_UNSCALED, LmError)
 
+
+
+class _NotBuilt:
+    """In _native's place where it cannot be imported: the calls that need it raise that."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"_native.so ({self._why}); run `python -m fp8_gemms_b200.build`")
+
+
 try:
     from . import _native
+    _native.use_error(LmError)
 except ImportError as e:
-    raise ImportError(f"_native.so ({e}); run `python -m fp8_gemms_b200.build`") from e
+    _native = _NotBuilt(str(e))
 
 
 def _dev(t):
@@ -364,9 +377,6 @@ def linear_fwd_bwd(X, W, dY, stream=None):
 # _native (csrc/binding.cpp) checks the arguments, allocates what is not given and makes
 # the C call on the current stream of the tensors' device.  stream: a torch.cuda.Stream
 # to run on instead, where the outputs and workspaces are allocated too.
-_native.use_error(LmError)
-
-
 def _call(fn, stream, *args):
     if stream is None:
         return fn(*args)
