@@ -375,13 +375,19 @@ def linear_fwd_bwd(X, W, dY, stream=None):
 
 # ------------------------------------------------- operators between the GEMMs
 # _native (csrc/binding.cpp) checks the arguments, allocates what is not given and makes
-# the C call on the current stream of the tensors' device.  stream: a torch.cuda.Stream
-# to run on instead, where the outputs and workspaces are allocated too.
+# the C call on the current stream of the tensors' device.  stream: a torch.cuda.Stream or a
+# raw handle (0: the default stream) to run on instead, where the outputs and workspaces are
+# allocated too.
 def _call(fn, stream, *args):
     if stream is None:
         return fn(*args)
-    first = args[0] if isinstance(args[0], torch.Tensor) else args[0][0]
-    if stream.device != first.device:
+    x = next((t for t in args if isinstance(t, torch.Tensor) and t.is_cuda), None)
+    if x is None:
+        return fn(*args)  # which refuses it: each call has a tensor that has to be on a GPU
+    if not hasattr(stream, "device"):
+        handle = getattr(stream, "cuda_stream", stream)
+        stream = torch.cuda.ExternalStream(handle, device=x.device)
+    elif stream.device != x.device:
         raise LmError(1, f"{fn.__name__}: the stream is of another device")
     with torch.cuda.stream(stream):
         return fn(*args)
