@@ -183,8 +183,9 @@ __device__ __forceinline__ void row_moments(int lane, int warp, int warps, float
         s = (float)(sum * inv_cols);
         const int left = cols - w * each;  // columns of warp w
         const float n = (float)(left < each ? left : each);
+        // divided before it is squared: d^2 is up to n times what is added
         const float d = mine.x - n * s;
-        q = left > 0 ? mine.y + __fdividef(d * d, n) : 0.f;
+        q = left > 0 ? __fmaf_rn(__fdividef(d, n), d, mine.y) : 0.f;
 #pragma unroll
         for (int o = kSpan / 2; o > 0; o >>= 1) q += __shfl_xor_sync(0xFFFFFFFFu, q, o);
     };

@@ -219,8 +219,8 @@ typedef enum { LM_DTYPE_BF16 = 0, LM_DTYPE_F32 = 1 } lm_dtype;
  *   m = mean_c X[r][c],  v = mean_c (X[r][c] - m)^2,  rstd = 1 / sqrt(v + eps)
  *   Y[r][c] = (X[r][c] - m) rstd weight[c] + bias[c]
  *
- * Sums in fp32, the variance from the centred values; Y is rounded once.  (So the
- * squares of a row's centred values have to fit fp32, and for the backward
+ * Sums in fp32, the variance from the centred values; Y is rounded once.  (So a row's
+ * sum and that of its centred values' squares have to fit fp32, and for the backward
  * 1 / rstd^2 = v + eps has to be a normal fp32, 1.2e-38 or more.)
  * X, Y: [rows x cols] with row strides ldx, ldy (elements, >= cols); weight,
  * bias: [cols], each may be NULL (1 and 0); mean, rstd: fp32 [rows] for the
