@@ -1024,6 +1024,7 @@ lm_status fwd(FwdArgs a, lm_dtype dtype, bool drop, lm_stream_t stream) {
     if (!aligned_to(a.mean, 4) || !aligned_to(a.rstd, 4) || !aligned_to(a.amax, 4))
         return LM_ERR_ALIGNMENT;
     if (a.rows == 0) return LM_OK;
+    if (share_bytes(a.mean, a.rstd, 4 * a.rows)) return LM_ERR_INVALID_ARG;
     a.inv_cols = 1.0 / (double)a.cols;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool bf16 = dtype == LM_DTYPE_BF16;
@@ -1061,6 +1062,8 @@ lm_status bwd(BwdArgs a, lm_dtype dtype, bool drop, void* dweight, void* dbias, 
     if (!aligned_to(dweight, size) || !aligned_to(dbias, size) || !aligned16(workspace) ||
         !aligned_to(a.mean, 4) || !aligned_to(a.rstd, 4))
         return LM_ERR_ALIGNMENT;
+    // two blocks would write, or add to, the same elements
+    if (a.rows > 0 && share_bytes(dweight, dbias, size * a.cols)) return LM_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     float* part = static_cast<float*>(workspace);
     a.inv_cols = 1.0 / (double)a.cols;

@@ -52,6 +52,12 @@ inline bool in_place_or_apart(const RowTensor& out, const RowTensor& in, int64_t
     return !out.p || out.p != in.p || rows <= 1 || out.ld == in.ld;
 }
 
+// Whether two vectors of n bytes each have any in common (a NULL one has none).
+inline bool share_bytes(const void* a, const void* b, int64_t n) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    return a && b && (p < q ? q - p : p - q) < (uintptr_t)n;
+}
+
 // The dropout of probability p: halfwords below round(p 2^16) are dropped.
 inline lm_status dropout_args(double p, const uint64_t* rng, uint64_t offset, Dropout* d) {
     if (!(p >= 0.0 && p <= 1.0) || !rng) return LM_ERR_INVALID_ARG;

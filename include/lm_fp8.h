@@ -224,7 +224,7 @@ typedef enum { LM_DTYPE_BF16 = 0, LM_DTYPE_F32 = 1 } lm_dtype;
  * 1 / rstd^2 = v + eps has to be a normal fp32, 1.2e-38 or more.)
  * X, Y: [rows x cols] with row strides ldx, ldy (elements, >= cols); weight,
  * bias: [cols], each may be NULL (1 and 0); mean, rstd: fp32 [rows] for the
- * backward pass, each may be NULL.
+ * backward pass, each may be NULL, apart from one another.
  * amax_out: device fp32 or NULL.  If non-NULL it is max-reduced (atomically,
  *   order independent) with max |Y|, NaN above everything, so that
  *   lm_fp8_amax_scale_cast can take it as amax_in and skip its reduction pass.
@@ -248,8 +248,8 @@ LM_API size_t lm_layernorm_workspace_size(int64_t rows, int64_t cols);
  *   dX = rstd (g - mean_c g - h mean_c(g h))
  *   dweight[c] = sum_r dY h,  dbias[c] = sum_r dY
  * mean, rstd: as the forward wrote them.  dweight, dbias: [cols] of the
- * tensors' type, or fp32 accumulators with LM_NORM_ACCUMULATE_WGRAD; either
- * may be NULL, and with both NULL no workspace is needed.  The sums over the
+ * tensors' type, or fp32 accumulators with LM_NORM_ACCUMULATE_WGRAD, apart from one
+ * another; either may be NULL, and with both NULL no workspace is needed.  The sums over the
  * rows have a fixed order: the same inputs give the same bits.
  * workspace: device scratch of >= lm_layernorm_workspace_size bytes, 16-byte
  *   aligned.  Calls that share a workspace must not overlap on the GPU.

@@ -69,3 +69,27 @@ def test_work_on_a_raw_handle_is_on_that_stream():
     want = api.layernorm(x, w)[0]
     torch.cuda.synchronize()
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_weight_gradients_side_by_side_in_one_buffer(accumulate):
+    """One behind the other they are as elsewhere; with elements in common, refused."""
+    from fp8_gemms_b200 import api
+    dy, x, w = draw((40, 264), BF, 1), draw((40, 264), BF, 2), vector(264, BF, 3)
+    _, mean, rstd = api.layernorm(x, w)
+    buf = torch.ones(2 * 264 + 8, dtype=torch.float32 if accumulate else BF, device="cuda")
+
+    def back(dw, db):
+        return api.layernorm_backward(dy, x, w, mean, rstd, dweight=dw, dbias=db,
+                                      accumulate=accumulate)
+    want = [t.clone() for t in back(buf[:264].clone(), buf[264:528].clone())]
+    got = back(buf[:264], buf[264:528])
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert (buf[528:] == 1).all()
+    before = buf.clone()
+    for dw, db in ((0, 0), (8, 0), (0, 263), (264, 1)):
+        with pytest.raises(api.LmError) as e:
+            back(buf[dw:dw + 264], buf[db:db + 264])
+        assert e.value.status == 1
+    assert torch.equal(buf, before)
