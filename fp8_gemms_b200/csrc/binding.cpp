@@ -69,9 +69,13 @@ bool truth(PyObject* o) {
     if (v < 0) throw python_error();
     return v;
 }
+// Any integer, as also `start` of rope() is taken (Python's, numpy's, a tensor's).
 uint64_t unsigned64(const char* what, PyObject* o) {
-    const unsigned long long v = PyLong_AsUnsignedLongLong(o);
-    if (v == (unsigned long long)-1 && PyErr_Occurred()) {
+    THPObjectPtr i(PyNumber_Index(o));
+    const unsigned long long v = i ? PyLong_AsUnsignedLongLong(i.get()) : 0;
+    if (PyErr_Occurred()) {
+        if (!PyErr_ExceptionMatches(PyExc_TypeError) && !PyErr_ExceptionMatches(PyExc_OverflowError))
+            throw python_error();
         PyErr_Clear();
         refuse(what, "offset is an unsigned 64-bit integer");
     }

@@ -1,4 +1,5 @@
 """What the row operators' and rotary calls take for a stream and for whole numbers."""
+import numpy as np
 import pytest
 import torch
 
@@ -93,3 +94,14 @@ def test_weight_gradients_side_by_side_in_one_buffer(accumulate):
             back(buf[dw:dw + 264], buf[db:db + 264])
         assert e.value.status == 1
     assert torch.equal(buf, before)
+
+
+@pytest.mark.parametrize("kind", [np.int64, np.uint64, torch.tensor])
+def test_offsets_of_any_integer_type(kind):
+    from fp8_gemms_b200 import api
+    x, rng = draw((9, 80), BF, 1), api.dropout_rng(5)
+    assert torch.equal(api.dropout_add(x, 0.5, rng, offset=kind(3)), api.dropout_add(x, 0.5, rng, offset=3))
+    for bad in (3.0, "3", -1, 1 << 64, None):
+        with pytest.raises(api.LmError) as e:
+            api.dropout_add(x, 0.5, rng, offset=bad)
+        assert e.value.status == 1
