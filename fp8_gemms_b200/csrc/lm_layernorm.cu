@@ -28,6 +28,7 @@
 #include <type_traits>
 
 #include "lm_chunk.cuh"
+#include "lm_device_once.h"
 #include "lm_internal.h"
 #include "lm_philox.cuh"
 #include "lm_rows.h"
@@ -896,16 +897,14 @@ Plan plan(int64_t rows, int warps, int threads, int sms, int shared, int row, in
     return p;
 }
 
-// Allows a kernel kSmemBytes of shared memory, once a device (done: by device).
+// Allows a kernel kSmemBytes of shared memory, once a device.
 template <typename K>
-bool allow_smem(K kernel, bool (&done)[64]) {
+bool allow_smem(K kernel, DeviceOnce& once) {
     int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
-    if (!done[dev] && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           kSmemBytes) != cudaSuccess)
-        return false;
-    done[dev] = true;
-    return true;
+    return cudaGetDevice(&dev) == cudaSuccess && once.run(dev, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kSmemBytes) == cudaSuccess;
+    });
 }
 
 // wc: chunks of 256 columns.  A warp takes four, which leaves the least to add up between
@@ -947,11 +946,11 @@ bool run_bwd(const BwdArgs& a, int64_t wc, int sms, float* part, cudaStream_t s,
     const int sums = p.groups > 1 ? 32 * warps * NCH * kChunk * 2 * (int)sizeof(float) : 0;
     if (p.bytes < sums) p.bytes = sums;
     *parts = 0;
-    static bool done[2][64] = {};
+    static DeviceOnce once[2];
     const bool full = VEC && a.cols % (NCH * kWarpCols) == 0;
     auto kernel = full ? norm_bwd_kernel<T, VEC, NCH, DROP, VEC>
                        : norm_bwd_kernel<T, VEC, NCH, DROP, false>;
-    if (!allow_smem(kernel, done[full])) return true;
+    if (!allow_smem(kernel, once[full])) return true;
     kernel<<<p.grid, p.threads, p.bytes, s>>>(a, warps, p.stages, part);
     if (launch_status() == LM_OK) *parts = p.grid;
     return true;
