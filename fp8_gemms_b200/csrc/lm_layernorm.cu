@@ -380,7 +380,7 @@ struct Group {
     }
 };
 
-// Sums of two values over a group of at most 32 warps, the same in every thread.  Lanes
+// Sums of two values over a group of at most 16 warps, the same in every thread.  Lanes
 // 0..15 go on with the first value and 16..31 with the second after one exchange.
 // `buf`: two floats for each warp of the group, others than the call before used.
 __device__ __forceinline__ void group_sum2(const Group& g, float* buf, float& a, float& b) {
@@ -396,7 +396,6 @@ __device__ __forceinline__ void group_sum2(const Group& g, float* buf, float& a,
         const float* const mine = buf + (upper ? g.warps : 0);
         const int k = g.lane & 15;
         v = k < g.warps ? mine[k] : 0.f;
-        if (g.warps > 16) v += k + 16 < g.warps ? mine[k + 16] : 0.f;
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     }
@@ -408,6 +407,7 @@ __device__ __forceinline__ void group_sum2(const Group& g, float* buf, float& a,
 // Threads of a backward block, at most: 128 registers each, of which the sums take up to
 // 64.
 constexpr int kBwdThreads = 512;
+static_assert(kBwdThreads <= 16 * 32, "group_sum2 adds up 16 warps");
 
 // The backward pass, every tensor read once for dx and the weight gradients.  A thread
 // keeps its NCH chunks' sums over its rows in registers; at the end the block adds its
@@ -420,7 +420,7 @@ template <typename T, bool VEC, int NCH, bool DROP, bool FULL>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     norm_bwd_kernel(const BwdArgs a, int warps, int stages, float* part) {
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ float buf[2 * 64];
+    __shared__ float buf[2 * 32];
     constexpr int NT = DROP ? 3 : 2;
     constexpr int kSlot = Slots<T>::kBytes, kRow = NT * NCH * kSlot;  // of a warp
     constexpr int kSize = sizeof(typename Elem<T>::raw), kNext = kWarpCols * kSize;
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         float c1 = lo_of(s1) + hi_of(s1), c2 = (lo_of(s2) + hi_of(s2)) * rstd;
         group_sum2(g, buf + mine, c1, c2);
-        mine ^= 64;
+        mine ^= 32;
         if (!kAgain) as_stored(d), as_stored(c), as_stored(w);
         // dx = rstd g - rstd c1 - (x - mean) rstd (rstd c2)
         const float per = (float)a.inv_cols * rstd;
