@@ -410,13 +410,20 @@ def _refuse(what, why, status=1):
     raise LmError(status, f"{what}: {why}")
 
 
+def _check_device(what, device):
+    # the launch, its stream and the multiprocessor count are those of the current device
+    if device != torch.cuda.current_device():
+        _refuse(what, "the tensors' device is not the current one")
+
+
 def _check_rows(what, x, *others):
     """x and `others` (each may be None): [rows x cols] CUDA tensors of one type
-    and device whose columns are adjacent.  Returns (rows, cols, lm_dtype, device index)
+    on the current device whose columns are adjacent.  Returns (rows, cols, lm_dtype, device index)
     and the row strides (0 for None)."""
     shape, dtype, device = x.shape, x.dtype, x.get_device()
     if len(shape) != 2 or device < 0:
         _refuse(what, "a 2-D CUDA tensor is wanted")
+    _check_device(what, device)
     code = _DTYPES.get(dtype)
     if code is None:
         _refuse(what, f"{dtype} is not supported", 4)
@@ -542,6 +549,7 @@ def lm_rope(xs, ys, inv_freq, positions=None, start=0, magnitude=1.0, flags=0, s
         _refuse("lm_rope", "one or two 4-D CUDA tensors and as many outputs are wanted")
     batch, seq, _, head_dim = xs[0].shape
     dtype, device = xs[0].dtype, xs[0].get_device()
+    _check_device("lm_rope", device)
     code = _DTYPES.get(dtype)
     if code is None:
         _refuse("lm_rope", f"{dtype} is not supported", 4)
