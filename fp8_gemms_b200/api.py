@@ -377,7 +377,8 @@ def linear_fwd_bwd(X, W, dY, stream=None):
 # _native (csrc/binding.cpp) checks the arguments, allocates what is not given and makes
 # the C call on the current stream of the tensors' device.  stream: a torch.cuda.Stream or a
 # raw handle (0: the default stream) to run on instead, where the outputs and workspaces are
-# allocated too.
+# allocated too.  An output that is given may be an input itself where the C interface allows
+# it (the same pointer and strides), and else shares no element with a tensor of the call.
 def _call(fn, stream, *args):
     if stream is None:
         return fn(*args)
@@ -395,8 +396,9 @@ def _call(fn, stream, *args):
 
 def layernorm(x, weight=None, bias=None, eps=1e-5, out=None, amax_out=None, stream=None):
     """Layer norm of [rows x cols] bf16 or fp32.  Returns (y, mean, rstd), the
-    statistics fp32 [rows] for layernorm_backward.  amax_out: a zeroed fp32
-    that receives max |y|, the amax_in of a following cast()."""
+    statistics fp32 [rows] for layernorm_backward.  amax_out: a zeroed fp32 [1]
+    that receives max |y|, the amax_in of a following cast() (Linear and the MLP
+    blocks take no amax and reduce their input themselves)."""
     return _call(_native.layernorm, stream, x, weight, bias, eps, out, amax_out)
 
 
@@ -410,8 +412,10 @@ def layernorm_backward(dy, x, weight, mean, rstd, out=None, dweight=None, dbias=
 
 def dropout_rng(seed, offset=0, device="cuda"):
     """The device {seed, offset} that the dropout calls read.  A training loop
-    adds to rng[1] between steps (also between replays of a captured graph);
-    calls of one step differ by their `offset` argument."""
+    adds to rng[1] between steps (also between replays of a captured graph), and
+    calls of one step differ by their `offset` argument.  The two are added, so
+    with offsets 0 to n - 1 a step advances rng[1] by n or more: by less, a call
+    gets the mask that another had the step before."""
     signed = [v - (1 << 64) if v >= 1 << 63 else v for v in (seed, offset)]
     return torch.tensor(signed, dtype=torch.int64, device=device)
 

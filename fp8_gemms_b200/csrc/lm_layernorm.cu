@@ -23,6 +23,11 @@
 //   forward        16384 x 4096 bf16 42.5 us (98%), 8192 x 8192 fp32 81 us (102%)
 //   backward       16384 x 4096 bf16 65 us (96%), of which the sum of the parts 4
 //   fused forward  8192 x 5120 bf16 52.5 us (99%); fused backward 8192 x 8192 108 (96%)
+// These are rows of whole 8-column accesses. Others (odd widths, rows at any alignment) go by
+// one element an access, a third to a half of a copy: 16384 x 4095 bf16 101 us forward, 146
+// backward, 168 and 260 fused. A row is read once up to 32,768 columns forward (others:
+// 16,384) and 16,384 backward (fp32 and others: 8,192; others of fp32 with dropout: 4,096); the
+// kernels for wider ones read it again for each sweep.
 // Over longer times the 1 kW limit lowers the SM clock to 1.6-1.8 GHz and all take 3-12%
 // longer, the copy 3%.
 #include <type_traits>
@@ -162,7 +167,8 @@ constexpr int kManyBytes = 160 * 1024;
 // and centred squares q_w in warp w, the row has mean m = sum s_w / n and centred
 // squares sum q_w + n_w (s_w / n_w - m)^2, so one exchange does for both.  `buf`: a
 // float2 for each warp; exchange(): a barrier of the row's warps.  The mean is a
-// product in fp64: exact where the mean is, as of a constant row.
+// product in fp64, so of the sum's value it is rounded once: a constant bf16 row, whose sums
+// are exact up to 2^16 columns, has its value for a mean.
 template <typename Exchange>
 __device__ __forceinline__ void row_moments(int lane, int warp, int warps, float2* buf, int cols,
                                             int each, double inv_cols, float& s, float& q,

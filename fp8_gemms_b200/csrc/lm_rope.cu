@@ -17,7 +17,7 @@
 // shared memory spent their time at barriers and behind 100 registers a thread (16384 tokens, 24 + 8
 // heads of 128, bf16: 93 us; now 43.5 us, 96% of what a copy reaches).  One token of 64
 // sequences takes 2.5 us: the latency of positions, angles and one access.  Where
-// rot_dim / 2 is odd the accesses are scalar (rot_dim 50 of 128: 113 us), where it is no
+// rot_dim / 2 is odd the accesses are scalar (rot_dim 50 of 128: 111 us), where it is no
 // multiple of 8 two elements wide (100 of 100: 48 us, 34 of them the bytes; fp32 68 of 68).
 #include <type_traits>
 
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(32 * kWarps) rope_kernel(const RopeArgs a, con
         auto fetch = [&](int h) {
             if (!works || h >= h1) return;
             // behind the last head the last one again: a test for each would part the loads
-            // (16384 tokens, 24 + 8 heads of 100, fp32: 131 us instead of 68; 64 tokens lose, bf16 3.5
+            // (16384 tokens, 24 + 8 heads of 100, fp32: 131 us instead of 68; 64 tokens lose, bf16 3.3
             // instead of 2.9, and one test at the fifth head costs 80)
 #pragma unroll
             for (int k = 0; k < kAtOnce; ++k) {

@@ -220,8 +220,9 @@ typedef enum { LM_DTYPE_BF16 = 0, LM_DTYPE_F32 = 1 } lm_dtype;
  *   Y[r][c] = (X[r][c] - m) rstd weight[c] + bias[c]
  *
  * Sums in fp32, the variance from the centred values; Y is rounded once.  (So a row's
- * sum and that of its centred values' squares have to fit fp32, and for the backward
- * 1 / rstd^2 = v + eps has to be a normal fp32, 1.2e-38 or more.)
+ * sum and that of its centred values' squares have to fit fp32; for the backward
+ * 1 / rstd^2 = v + eps has to be a normal fp32, 1.2e-38 or more, and rstd^2 mean_c(g h)
+ * has to fit.)
  * X, Y: [rows x cols] with row strides ldx, ldy (elements, >= cols); weight,
  * bias: [cols], each may be NULL (1 and 0); mean, rstd: fp32 [rows] for the
  * backward pass, each may be NULL, apart from one another.
@@ -277,6 +278,9 @@ LM_API lm_status lm_layernorm_bwd(const void* dY, int64_t lddy, const void* X, i
  * p in [0, 1].  rng: device {seed, offset}, read by the kernel, so that a
  *   captured graph takes a new mask when the caller advances the offset; o is that
  *   offset plus the argument `offset` (the layer's number, for instance).
+ *   Calls with equal o share a mask: where the calls of a step take `offset` 0 to n - 1, the
+ *   offset on the device is advanced by n or more a step, or a call gets the mask that
+ *   another had the step before.
  * X, residual, Y: [rows x cols] with row strides; alignment as
  *   lm_layernorm_fwd.  Y may be X or residual (same pointer and stride).
  */
