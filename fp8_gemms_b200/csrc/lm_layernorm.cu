@@ -24,8 +24,8 @@
 //   backward       16384 x 4096 bf16 65 us (96%), of which the sum of the parts 4
 //   fused forward  8192 x 5120 bf16 52.5 us (99%); fused backward 8192 x 8192 108 (96%)
 // These are rows of whole 8-column accesses. Others (odd widths, rows at any alignment) go by
-// one element an access, a third to a half of a copy: 16384 x 4095 bf16 101 us forward, 146
-// backward, 168 and 260 fused. A row is read once up to 32,768 columns forward (others:
+// one element an access, 40 to 50% of a copy: 16384 x 4095 bf16 102 us forward, 148
+// backward, 166 and 257 fused. A row is read once up to 32,768 columns forward (others:
 // 16,384) and 16,384 backward (fp32 and others: 8,192; others of fp32 with dropout: 4,096); the
 // kernels for wider ones read it again for each sweep.
 // Over longer times the 1 kW limit lowers the SM clock to 1.6-1.8 GHz and all take 3-12%
